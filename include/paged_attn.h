@@ -327,6 +327,100 @@ int pa_decode_int8(const void* q, const void* k_codes, const void* v_codes, cons
                    size_t workspace_bytes, int num_partitions_or_0, void* out, void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* INT4 KV cache (P1 s4.3: KV-cache compression in the tuning checklist).   */
+/* The pages fix no format; this one: every (token, KV head) row of         */
+/* head_dim values x (16-bit, type dtype) is cut into n = head_dim / 64     */
+/* groups of 64.  A group is 64 unsigned 4-bit codes with a scale s and a   */
+/* zero point z, both in the 16-bit type, and stands for s * (code + z):    */
+/*   lo = min x, hi = max x,  s = round16(hi / 15 - lo / 15),               */
+/*   z = round16(lo / s),     code = clamp(rint(x * (1 / s) - z), 0, 15)    */
+/* in fp32 (IEEE division, multiply, subtract, each rounded), round16 and   */
+/* rint to nearest even.  Where s < 2^-126 (values all alike, or nearer     */
+/* than the type's scale can say): s = |lo|, z = sign(lo), codes 0.  The    */
+/* codes are taken against the rounded s and z, so those roundings cost at  */
+/* most a shifted range, never an inconsistent value.  4.5 bits per value.  */
+/* Finite values of any size are in the format; a NaN or infinity spoils    */
+/* its own group only.                                                      */
+/* Layout: codes k_codes, v_codes uint8 [num_blocks][Hkv][block_size][D/2]  */
+/* (head-major, unlike the 16-bit and int8 caches: one head's rows of a     */
+/* block are one contiguous run that one bulk copy fetches).  A row is D/8  */
+/* 4-byte words of 8 codes, lowest nibble first; word j holds values        */
+/* 8 * (j div n) .. + 7 of group j mod n (the groups' words alternate, so   */
+/* that a thread's 16-byte load holds codes of every group).  Parameters    */
+/* k_params, v_params [num_blocks][Hkv][block_size][n][2] = (s, z), 16-bit  */
+/* (dtype).  All four 16-byte aligned.                                      */
+/* The 16-bit type of the parameters is the model's: every dtype argument   */
+/* below is the type of q, k, v, out AND of the parameters.                 */
+/*                                                                          */
+/* pa_write_kv_int4: for every t with slot = slot_mapping[t] >= 0, quantise */
+/* k[t][h] and v[t][h] ([num_tokens][Hkv][D]) into row slot % bs of block   */
+/* slot / bs.  k_out, v_out (each may be NULL): [num_tokens][Hkv][D], get   */
+/* the rows as the cache now holds them, s * (code + z) rounded to the type */
+/* (what later reads see, for the attention of the same step); they may be  */
+/* k and v themselves.  Rows of a token without a slot are left alone       */
+/* everywhere; a slot >= num_blocks * block_size writes nothing and sets    */
+/* PA_ERRBIT_INDEX.  num_tokens * Hkv * D / 8 must be below 2^31            */
+/* (PA_ERR_UNSUPPORTED otherwise).  Launch rules of pa_write_kv.            */
+/* ------------------------------------------------------------------------ */
+int pa_write_kv_int4(const void* k, const void* v, const int64_t* slot_mapping, int num_tokens, void* k_codes,
+                     void* v_codes, void* k_params, void* v_params, void* k_out, void* v_out, int num_blocks,
+                     int block_size, int num_kv_heads, int head_dim, int dtype, void* stream);
+
+/* pa_rope_write_kv_int4: pa_rope_write_kv into the INT4 cache: q turned     */
+/* into q_out, k turned, rounded to the type and quantised (bit for bit     */
+/* what pa_rope_write_kv followed by pa_write_kv_int4 of its k rows gives), */
+/* v quantised.  Arguments, refusals and error bits of the two; a position  */
+/* out of range leaves every row of its token unwritten.  k_out, v_out as   */
+/* above (k_out: the turned rows as held).  num_tokens * (num_q_heads +     */
+/* 2 * Hkv) * D / 16 must be below 2^31.                                    */
+int pa_rope_write_kv_int4(const void* q, void* q_out, const void* k, const void* v, const int64_t* positions,
+                          const float* cos_table, const float* sin_table, int max_position,
+                          const int64_t* slot_mapping, int num_tokens, int num_q_heads, void* k_codes, void* v_codes,
+                          void* k_params, void* v_params, void* k_out, void* v_out, int num_blocks, int block_size,
+                          int num_kv_heads, int head_dim, int dtype, void* stream);
+
+/* Copy-on-write for the INT4 cache: for each pair i, block pairs[2i+1] of  */
+/* the codes and parameters becomes a bitwise copy of block pairs[2i].  A   */
+/* source may repeat; destinations must be distinct from one another and    */
+/* from every source.  An id out of range skips its pair and sets           */
+/* PA_ERRBIT_INDEX.                                                         */
+int pa_copy_blocks_int4(const int32_t* pairs, int num_pairs, void* k_codes, void* v_codes, void* k_params,
+                        void* v_params, int num_blocks, int block_size, int num_kv_heads, int head_dim, void* stream);
+
+/* Blocks of the INT4 cache expanded into a 16-bit paged cache (dtype,      */
+/* [num_dst_blocks][block_size][Hkv][D]): for each pair i, block pairs[2i+1]*/
+/* of k_cache and v_cache gets the values of block pairs[2i], rounded to    */
+/* the type.  This is how pa_prefill_chunk and the cascade, which read      */
+/* 16-bit caches, attend over a context held in 4 bits.  Destinations must  */
+/* be distinct.  An id out of range skips its pair and sets PA_ERRBIT_INDEX.*/
+int pa_load_blocks_int4(const int32_t* pairs, int num_pairs, const void* k_codes, const void* v_codes,
+                        const void* k_params, const void* v_params, int num_blocks, void* k_cache, void* v_cache,
+                        int num_dst_blocks, int block_size, int num_kv_heads, int head_dim, int dtype, void* stream);
+
+/* pa_decode_int4: pa_decode over the INT4 cache.  Computes                 */
+/*   out[b][h] = sum_t softmax_t(scale * <q[b][h], Kd_b[t]>) Vd_b[t]        */
+/* with Kd, Vd the rows s * (code + z) of KV head h/G; q and out are 16-bit */
+/* (dtype), scores, softmax state and accumulators fp32.  context_lens[b]   */
+/* == 0 gives out[b] = 0.  lse_out: fp32 [batch][Hq] (4-byte aligned) or    */
+/* NULL; as in pa_decode_lse.  Argument checks, return codes, workspace     */
+/* rules and launch behaviour of pa_decode; the workspace size comes from   */
+/* pa_decode_int4_workspace_size (or pa_decode_int4_plan: grid = CTAs,      */
+/* max_pieces = partial results the workspace holds per head of a group).   */
+/* Internally q enters as fp16 after an exact power-of-two prescale (its    */
+/* largest magnitude lands in [2^14, 2^15)) and the softmax weights enter   */
+/* the V product times the V scale, as fp16; q elements below 2^-28 of the  */
+/* group's largest lose precision.                                          */
+int pa_decode_int4_plan(int batch, int num_q_heads, int num_kv_heads, int head_dim, int max_context_len,
+                        int num_partitions_or_0, int* grid_out, int* max_pieces_out, size_t* workspace_bytes_out);
+size_t pa_decode_int4_workspace_size(int batch, int num_q_heads, int num_kv_heads, int head_dim,
+                                     int max_context_len, int num_partitions_or_0);
+int pa_decode_int4(const void* q, const void* k_codes, const void* v_codes, const void* k_params,
+                   const void* v_params, const int32_t* block_tables, int max_blocks_per_seq,
+                   const int32_t* context_lens, int batch, int num_q_heads, int num_kv_heads, int head_dim,
+                   int block_size, int num_blocks, int max_context_len, float scale, int dtype, void* workspace,
+                   size_t workspace_bytes, int num_partitions_or_0, void* out, float* lse_out, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Decode with the context split across devices (P3 s1.1 / s3.1 DCP: each  */
 /* device attends over the part of the KV cache it holds; the intermediate */
 /* results are gathered from all devices (AllGather) and combined).         */

@@ -13,6 +13,8 @@ Calls (see the header for exact semantics):
 * ``decode``         - one-token paged attention, split-K with the merge in the same kernel
 * ``prefill_chunk``  - causal chunked-prefill attention over the paged cache
 * ``write_kv_int8``, ``decode_int8``, ``copy_blocks_int8`` - the same over an INT8 cache (codes + fp32 scales)
+* ``write_kv_int4``, ``rope_write_kv_int4``, ``decode_int4``, ``copy_blocks_int4``, ``load_blocks_int4`` - the same
+  over an INT4 cache (groups of 64 codes with a 16-bit scale and zero point), and its blocks expanded to 16 bits
 * ``BlockPool``      - host block pool: blocks, block tables, reference counts
 """
 
@@ -28,7 +30,8 @@ __all__ = ["PagedAttnError", "PoolOutOfBlocks", "BlockPool", "write_kv", "copy_b
            "decode_static_scratch",
            "prefill_chunk", "device_error", "lib", "LIB_PATH", "replay_ops", "version",
            "write_kv_int8", "copy_blocks_int8", "decode_int8", "decode_int8_plan", "decode_lse", "merge_attn_states",
-           "decode_cascade", "decode_cascade_workspace_size", "copy_async"]
+           "decode_cascade", "decode_cascade_workspace_size", "copy_async", "write_kv_int4", "rope_write_kv_int4",
+           "decode_int4", "decode_int4_plan", "copy_blocks_int4", "load_blocks_int4"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libpaged_attn.so")
 
@@ -78,6 +81,15 @@ _SIGS = {
     "pa_decode_int8_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i]),
     "pa_decode_int8": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _i, _vp, _sz, _i,
                             _vp, _vp]),
+    "pa_write_kv_int4": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp]),
+    "pa_rope_write_kv_int4": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp,
+                                   _i, _i, _i, _i, _i, _vp]),
+    "pa_copy_blocks_int4": (_i, [_vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp]),
+    "pa_load_blocks_int4": (_i, [_vp, _i, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _vp]),
+    "pa_decode_int4_plan": (_i, [_i, _i, _i, _i, _i, _i, _ip, _ip, ctypes.POINTER(_sz)]),
+    "pa_decode_int4_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "pa_decode_int4": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _i, _vp, _sz, _i,
+                            _vp, _vp, _vp]),
     "pa_pool_create": (_vp, [_i, _i, _i32p]),
     "pa_pool_destroy": (None, [_vp]),
     "pa_seq_alloc": (_i, [_vp, _i64, _i]),
@@ -544,6 +556,148 @@ def decode_int8(q, k_codes, v_codes, k_scales, v_scales, block_tables, context_l
                               _ptr(block_tables), int(block_tables.shape[1]), _ptr(context_lens), B, Hq, Hkv, D, bs,
                               NB, int(max_context_len), float(scale), _dtype_code(q), _ptr(workspace), ws_bytes,
                               int(num_partitions), _ptr(out), _stream_handle(stream)), "pa_decode_int8")
+    return out
+
+
+# ---------------------------------------------------------------------------------------------- INT4 cache
+def _int4_caches(k_codes, v_codes, k_params, v_params):
+    """Codes uint8 [NB, Hkv, bs, D/2] (both alike), parameters [NB, Hkv, bs, D/64, 2] (both alike, bf16 or fp16);
+    returns (NB, bs, Hkv, D)."""
+    torch = _torch()
+    cs, ps = k_codes.shape, k_params.shape
+    if (len(cs) == 4 and v_codes.shape == cs and k_codes.dtype == torch.uint8 == v_codes.dtype
+            and k_params.dtype == v_params.dtype and v_params.shape == ps and len(ps) == 5 and ps[:3] == cs[:3]
+            and ps[3] * 32 == cs[3] and ps[4] == 2):
+        _dtype_code(k_params)
+        return cs[0], cs[2], cs[1], cs[3] * 2
+    _want("k_codes", k_codes, dtype=torch.uint8, ndim=4)
+    _want("v_codes", v_codes, dtype=torch.uint8, shape=cs)
+    if cs[3] % 32:
+        raise ValueError(f"k_codes holds rows of {cs[3]} bytes; a row is head_dim / 2 bytes, a multiple of 32")
+    _dtype_code(k_params)
+    _want("k_params", k_params, shape=(cs[0], cs[1], cs[2], cs[3] // 32, 2))
+    _want("v_params", v_params, dtype=k_params.dtype, shape=ps)
+    raise AssertionError("cache check failed without a reason")
+
+
+def write_kv_int4(k, v, slot_mapping, k_codes, v_codes, k_params, v_params, k_out=None, v_out=None,
+                  stream=None) -> None:
+    """Quantise k, v [T, Hkv, D] (the parameters' dtype) into the INT4 cache rows of slot_mapping int64 [T]
+    (-1 = skip).  k_out, v_out (like k, v; they may be k, v): the rows as the cache now holds them."""
+    torch = _torch()
+    _contig(k, v, slot_mapping, k_codes, v_codes, k_params, v_params, k_out, v_out)
+    NB, bs, Hkv, D = _int4_caches(k_codes, v_codes, k_params, v_params)
+    T, dt = int(k.shape[0]) if k.dim() > 0 else -1, k_params.dtype
+    for name, x in (("k", k), ("v", v), ("k_out", k_out), ("v_out", v_out)):
+        if x is not None:
+            _want(name, x, dtype=dt, shape=(T, Hkv, D))
+    _want("slot_mapping", slot_mapping, dtype=torch.int64, shape=(T,))
+    _device(stream, k, v, slot_mapping, k_codes, v_codes, k_params, v_params, k_out, v_out)
+    _check(lib.pa_write_kv_int4(_ptr(k), _ptr(v), _ptr(slot_mapping), T, _ptr(k_codes), _ptr(v_codes), _ptr(k_params),
+                                _ptr(v_params), _ptr(k_out), _ptr(v_out), NB, bs, Hkv, D, _dtype_code(k_params),
+                                _stream_handle(stream)), "pa_write_kv_int4")
+
+
+def rope_write_kv_int4(q, k, v, positions, cos_table, sin_table, slot_mapping, k_codes, v_codes, k_params, v_params,
+                       q_out=None, k_out=None, v_out=None, stream=None):
+    """rope_write_kv into the INT4 cache: q and k turned by their positions' table rows, k and v quantised into
+    their slots.  Returns q_out (a new tensor unless given; q_out=q rotates in place).  k_out, v_out as in
+    write_kv_int4."""
+    torch = _torch()
+    if q_out is None:
+        q_out = torch.empty_like(q)
+    _contig(q, q_out, k, v, positions, cos_table, sin_table, slot_mapping, k_codes, v_codes, k_params, v_params, k_out,
+            v_out)
+    NB, bs, Hkv, D = _int4_caches(k_codes, v_codes, k_params, v_params)
+    dt = k_params.dtype
+    _want("q", q, dtype=dt, ndim=3)
+    T, Hq = int(q.shape[0]), int(q.shape[1])
+    _want("q", q, shape=(T, Hq, D))
+    _want("q_out", q_out, dtype=dt, shape=(T, Hq, D))
+    for name, x in (("k", k), ("v", v), ("k_out", k_out), ("v_out", v_out)):
+        if x is not None:
+            _want(name, x, dtype=dt, shape=(T, Hkv, D))
+    _want("positions", positions, dtype=torch.int64, shape=(T,))
+    _want("slot_mapping", slot_mapping, dtype=torch.int64, shape=(T,))
+    _want("cos_table", cos_table, dtype=torch.float32, ndim=2)
+    _want("cos_table", cos_table, shape=(cos_table.shape[0], D // 2))
+    _want("sin_table", sin_table, dtype=torch.float32, shape=cos_table.shape)
+    _device(stream, q, q_out, k, v, positions, cos_table, sin_table, slot_mapping, k_codes, v_codes, k_params,
+            v_params, k_out, v_out)
+    _check(lib.pa_rope_write_kv_int4(_ptr(q), _ptr(q_out), _ptr(k), _ptr(v), _ptr(positions), _ptr(cos_table),
+                                     _ptr(sin_table), int(cos_table.shape[0]), _ptr(slot_mapping), T, Hq,
+                                     _ptr(k_codes), _ptr(v_codes), _ptr(k_params), _ptr(v_params), _ptr(k_out),
+                                     _ptr(v_out), NB, bs, Hkv, D, _dtype_code(k_params), _stream_handle(stream)),
+           "pa_rope_write_kv_int4")
+    return q_out
+
+
+def copy_blocks_int4(pairs, k_codes, v_codes, k_params, v_params, stream=None) -> None:
+    """pairs int32 [n, 2] (src, dst) on the device: copy whole blocks of the INT4 codes and parameters."""
+    torch = _torch()
+    _contig(pairs, k_codes, v_codes, k_params, v_params)
+    NB, bs, Hkv, D = _int4_caches(k_codes, v_codes, k_params, v_params)
+    _want("pairs", pairs, dtype=torch.int32, ndim=2)
+    _want("pairs", pairs, shape=(pairs.shape[0], 2))
+    _device(stream, pairs, k_codes, v_codes, k_params, v_params)
+    _check(lib.pa_copy_blocks_int4(_ptr(pairs), int(pairs.shape[0]), _ptr(k_codes), _ptr(v_codes), _ptr(k_params),
+                                   _ptr(v_params), NB, bs, Hkv, D, _stream_handle(stream)), "pa_copy_blocks_int4")
+
+
+def load_blocks_int4(pairs, k_codes, v_codes, k_params, v_params, k_cache, v_cache, stream=None) -> None:
+    """pairs int32 [n, 2] (src, dst) on the device: expand block src of the INT4 cache into block dst of the
+    16-bit cache k_cache, v_cache [NB2, bs, Hkv, D] (the parameters' dtype), where prefill_chunk and
+    decode_cascade read."""
+    torch = _torch()
+    _contig(pairs, k_codes, v_codes, k_params, v_params, k_cache, v_cache)
+    NB, bs, Hkv, D = _int4_caches(k_codes, v_codes, k_params, v_params)
+    _want("k_cache", k_cache, dtype=k_params.dtype, ndim=4)
+    _want("k_cache", k_cache, shape=(k_cache.shape[0], bs, Hkv, D))
+    _want("v_cache", v_cache, dtype=k_params.dtype, shape=k_cache.shape)
+    _want("pairs", pairs, dtype=torch.int32, ndim=2)
+    _want("pairs", pairs, shape=(pairs.shape[0], 2))
+    _device(stream, pairs, k_codes, v_codes, k_params, v_params, k_cache, v_cache)
+    _check(lib.pa_load_blocks_int4(_ptr(pairs), int(pairs.shape[0]), _ptr(k_codes), _ptr(v_codes), _ptr(k_params),
+                                   _ptr(v_params), NB, _ptr(k_cache), _ptr(v_cache), int(k_cache.shape[0]), bs, Hkv, D,
+                                   _dtype_code(k_params), _stream_handle(stream)), "pa_load_blocks_int4")
+
+
+def decode_int4_plan(batch, num_q_heads, num_kv_heads, head_dim, max_context_len, num_partitions=0):
+    """(grid, max_pieces, workspace_bytes) of decode over the INT4 cache on the current device."""
+    gr, mp, ws = ctypes.c_int(), ctypes.c_int(), ctypes.c_size_t()
+    _check(lib.pa_decode_int4_plan(batch, num_q_heads, num_kv_heads, head_dim, max_context_len, num_partitions,
+                                   ctypes.byref(gr), ctypes.byref(mp), ctypes.byref(ws)), "pa_decode_int4_plan")
+    return gr.value, mp.value, ws.value
+
+
+def decode_int4(q, k_codes, v_codes, k_params, v_params, block_tables, context_lens, max_context_len: int,
+                scale: float, out=None, lse=None, workspace=None, num_partitions: int = 0, stream=None):
+    """Decode over the INT4 cache: q [B, Hq, D] in the parameters' dtype; returns out [B, Hq, D].  lse (float32
+    [B, Hq], optional) receives the log-sum-exp of each (sequence, head)'s scores, as decode_lse gives it."""
+    torch = _torch()
+    _contig(q, k_codes, v_codes, k_params, v_params, block_tables, context_lens, out, lse, workspace)
+    NB, bs, Hkv, D = _int4_caches(k_codes, v_codes, k_params, v_params)
+    _want("q", q, dtype=k_params.dtype, ndim=3)
+    B, Hq = int(q.shape[0]), int(q.shape[1])
+    _want("q", q, shape=(B, Hq, D))
+    _want("block_tables", block_tables, dtype=torch.int32, ndim=2)
+    _want("block_tables", block_tables, shape=(B, block_tables.shape[1]))
+    _want("context_lens", context_lens, dtype=torch.int32, shape=(B,))
+    if out is not None:
+        _want("out", out, dtype=q.dtype, shape=q.shape)
+    if lse is not None:
+        _want("lse", lse, dtype=torch.float32, shape=(B, Hq))
+    _device(stream, q, k_codes, v_codes, k_params, v_params, block_tables, context_lens, out, lse, workspace)
+    if out is None:
+        out = torch.empty_like(q)
+    if workspace is None:  # zero-filled once; every call leaves it zeroed again (a given one is checked by the library)
+        _, _, need = decode_int4_plan(B, Hq, Hkv, D, max_context_len, num_partitions)
+        workspace = torch.zeros(need, dtype=torch.uint8, device=q.device)
+    ws_bytes = workspace.numel() * workspace.element_size()
+    _check(lib.pa_decode_int4(_ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(k_params), _ptr(v_params),
+                              _ptr(block_tables), int(block_tables.shape[1]), _ptr(context_lens), B, Hq, Hkv, D, bs,
+                              NB, int(max_context_len), float(scale), _dtype_code(q), _ptr(workspace), ws_bytes,
+                              int(num_partitions), _ptr(out), _ptr(lse), _stream_handle(stream)), "pa_decode_int4")
     return out
 
 

@@ -12,6 +12,8 @@ extern "C" int pa__err_decode(unsigned int* out);
 extern "C" int pa__err_prefill(unsigned int* out);
 extern "C" int pa__err_rope(unsigned int* out);
 extern "C" int pa__err_int8(unsigned int* out);
+extern "C" int pa__err_int4(unsigned int* out);
+extern "C" int pa__err_decode_int4(unsigned int* out);
 
 extern "C" const char* pa_strerror(int status) {
   switch (status) {
@@ -40,14 +42,16 @@ extern "C" int pa_copy_async(void* dst, const void* src, size_t bytes, void* str
 extern "C" int pa_device_error(int* out) {
   if (!out) return PA_ERR_INVALID;
   if (cudaDeviceSynchronize() != cudaSuccess) return PA_ERR_CUDA;
-  unsigned int a = 0, b = 0, c = 0, d = 0, e = 0;
+  unsigned int a = 0, b = 0, c = 0, d = 0, e = 0, f = 0, g = 0;
   int s;
   if ((s = pa__err_write_kv(&a)) != PA_OK) return s;
   if ((s = pa__err_decode(&b)) != PA_OK) return s;
   if ((s = pa__err_prefill(&c)) != PA_OK) return s;
   if ((s = pa__err_rope(&d)) != PA_OK) return s;
   if ((s = pa__err_int8(&e)) != PA_OK) return s;
-  *out = (int)(a | b | c | d | e);
+  if ((s = pa__err_int4(&f)) != PA_OK) return s;
+  if ((s = pa__err_decode_int4(&g)) != PA_OK) return s;
+  *out = (int)(a | b | c | d | e | f | g);
   return PA_OK;
 }
 

@@ -1,0 +1,465 @@
+// INT4 KV cache: the quantising cache write (alone and behind the rotary
+// embedding), the block copy, and the expansion of blocks into a 16-bit cache.
+//
+// KV-cache compression is among the tuning steps of "Nano-vLLM-Ascend:
+// lightweight LLM inference framework for Ascend NPU", section 4.3; the pages
+// give no format.  The one built here cuts a row of D values (one token, one
+// KV head) into groups of 64; a group holds unsigned 4-bit codes, a scale s and
+// a zero point z (both in the 16-bit type of the values) and stands for
+// s * (code + z):
+//
+//   lo = min x;  hi = max x;  s = round16(hi / 15 - lo / 15);  z = round16(lo / s);
+//   code = clamp(rint(x * (1 / s) - z), 0, 15)
+//
+// in fp32, every operation rounded by itself (so another IEEE implementation
+// reaches the same codes).  The quotients are subtracted, not the values: hi -
+// lo can overflow, the difference of the quotients cannot.  s and z are rounded
+// before the codes are taken, so the rounding shifts the range the codes span
+// but adds nothing to a value's error.  s < 2^-126 (all values alike, or nearer
+// than the type can say; 1 / s would overflow): s = |lo|, z = sign(lo), codes 0.
+// One group never spans tokens: appending a token re-quantises nothing.
+//
+// Layout: codes [num_blocks][Hkv][block_size][D/2], parameters
+// [num_blocks][Hkv][block_size][D/64][2].  Word j (8 codes) of a row holds
+// values 8 * (j div n) .. of group j mod n, n = D/64.
+//
+// Work split of the write and of the expansion: D/16 threads per row, each with
+// 8 values of the first and 8 of the second half of the row.  That pair is what
+// a rotate-half embedding turns, a 16-byte vector of the input twice, and (at D
+// 128, where the halves are the groups) two neighbouring words of the stored
+// row; at D 64 it is words j and j + 4.
+
+#include "common.cuh"
+#include "host_common.h"
+
+PA_DEFINE_ERROR_WORD(pa__err_int4)
+
+namespace {
+
+using namespace pa;
+
+__device__ __forceinline__ uint4 ld_plain_v4(const void* p) {  // q and k may be overwritten in place
+  uint4 r;
+  asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+  return r;
+}
+
+template <int DT>
+__device__ __forceinline__ void unpack8(uint4 u, float* x) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = Elt<DT>::to_f2(w[i]);
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ uint4 pack8(const float* x) {
+  return make_uint4(Elt<DT>::from_f2(x[0], x[1]), Elt<DT>::from_f2(x[2], x[3]), Elt<DT>::from_f2(x[4], x[5]),
+                    Elt<DT>::from_f2(x[6], x[7]));
+}
+
+// Scale, zero point (as the 16-bit word pair s | z << 16) and reciprocal of a group with extremes lo, hi.
+template <int DT>
+__device__ __forceinline__ uint32_t group_params(float lo, float hi, float& s, float& z, float& inv) {
+  s = Elt<DT>::to_f2(Elt<DT>::from_f2(__fsub_rn(__fdiv_rn(hi, 15.f), __fdiv_rn(lo, 15.f)), 0.f)).x;
+  if (s >= 1.17549435e-38f) {
+    z = __fdiv_rn(lo, s);
+    inv = __fdiv_rn(1.f, s);
+  } else {
+    s = fabsf(lo);
+    z = lo > 0.f ? 1.f : (lo < 0.f ? -1.f : 0.f);
+    inv = 0.f;  // with the shift below every code is 0
+  }
+  const uint32_t w = Elt<DT>::from_f2(s, z);
+  z = Elt<DT>::to_f2(w).y;
+  return w;
+}
+
+// 8 values -> a word of 8 codes; x becomes the values that the codes stand for (unrounded).
+__device__ __forceinline__ uint32_t encode8(float* x, float s, float z, float inv) {
+  uint32_t word = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    int c = __float2int_rn(__fsub_rn(__fmul_rn(x[i], inv), z));
+    c = inv == 0.f ? 0 : min(15, max(0, c));
+    word |= (uint32_t)c << (4 * i);
+    x[i] = __fmul_rn(s, __fadd_rn((float)c, z));
+  }
+  return word;
+}
+
+__device__ __forceinline__ float min8(const float* x) {
+  return fminf(fminf(fminf(x[0], x[1]), fminf(x[2], x[3])), fminf(fminf(x[4], x[5]), fminf(x[6], x[7])));
+}
+__device__ __forceinline__ float max8(const float* x) {
+  return fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+}
+
+struct WriteArgs {
+  const uint4* q;  // rotary form only
+  uint4* q_out;
+  const uint4* k;
+  const uint4* v;
+  const int64_t* positions;
+  const float4* cos_t;
+  const float4* sin_t;
+  const int64_t* slots;
+  uint8_t* kc;
+  uint8_t* vc;
+  uint32_t* kp;
+  uint32_t* vp;
+  uint4* k_out;  // may be null
+  uint4* v_out;
+  int64_t num_slots, max_position;
+  int total;  // threads' items: tokens * (hq + 2 * hkv) * D / 16
+  int hq, hkv, block_size;
+};
+
+// Items: per token hq rows of q (rotary form), hkv rows of k, hkv rows of v; D/16 neighbouring threads a row.
+// Warps run whole iterations (the group extremes come from shuffles), threads past the end idle along.
+template <int DT, int D, bool ROPE>
+__global__ void __launch_bounds__(256) write_kv_int4_kernel(const WriteArgs a) {
+  // a decode launched after this may start its set-up now; it waits for this grid before it reads the cache
+  asm volatile("griddepcontrol.launch_dependents;");
+  // launched programmatically itself: wait for the preceding grid before reading inputs or writing slots
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int TPR = D / 16, NG = D / 64;
+  const int rows = a.hq + 2 * a.hkv;
+  for (int64_t base = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) & ~31ll; base < a.total;
+       base += (int64_t)gridDim.x * blockDim.x) {
+    const int i = (int)base + (threadIdx.x & 31);
+    const bool in = i < a.total;
+    const int row = in ? i / TPR : 0, j = i % TPR;
+    const int t = row / rows, r = row - t * rows;
+    const bool isq = ROPE && r < a.hq, isv = r >= a.hq + a.hkv;
+    const int h = isq ? r : (isv ? r - a.hq - a.hkv : r - a.hq);
+    bool live = in;
+    int64_t pos = 0, slot = 0;
+    if (ROPE && in) {
+      pos = __ldg(a.positions + t);
+      if (pos < 0 || pos >= a.max_position) {  // broken caller invariant: record once per token, write nothing
+        if (r == 0 && j == 0) PA_RECORD_ERROR(PA_ERRBIT_INDEX);
+        live = false;
+      }
+    }
+    if (live && !isq) {
+      slot = __ldg(a.slots + t);
+      if (slot >= a.num_slots && r == a.hq && j == 0) PA_RECORD_ERROR(PA_ERRBIT_INDEX);
+      live = slot >= 0 && slot < a.num_slots;
+    }
+    const int64_t src_row = isq ? (int64_t)t * a.hq + h : (int64_t)t * a.hkv + h;
+    const int64_t vec = src_row * (D / 8) + j;
+    float x1[8], x2[8];
+    if (live) {
+      const uint4* src = (isq ? a.q : (isv ? a.v : a.k)) + vec;
+      uint4 u1 = ld_plain_v4(src), u2 = ld_plain_v4(src + TPR);
+      unpack8<DT>(u1, x1);
+      unpack8<DT>(u2, x2);
+      if (ROPE && !isv) {
+        const int64_t tb = pos * (D / 8) + 2 * j;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const float4 c = __ldg(a.cos_t + tb + half), s = __ldg(a.sin_t + tb + half);
+          const float cv[4] = {c.x, c.y, c.z, c.w}, sv[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float p = x1[4 * half + e], w = x2[4 * half + e];
+            x1[4 * half + e] = fmaf(p, cv[e], -__fmul_rn(w, sv[e]));
+            x2[4 * half + e] = fmaf(w, cv[e], __fmul_rn(p, sv[e]));
+          }
+        }
+        u1 = pack8<DT>(x1);
+        u2 = pack8<DT>(x2);
+        if (isq) {
+          st_v4(a.q_out + vec, u1);
+          st_v4(a.q_out + vec + TPR, u2);
+        }
+        unpack8<DT>(u1, x1);  // the key as the 16-bit cache would hold it
+        unpack8<DT>(u2, x2);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x1[e] = x2[e] = 0.f;
+    }
+    float lo1 = min8(x1), hi1 = max8(x1), lo2 = min8(x2), hi2 = max8(x2);
+    if constexpr (NG == 1) {
+      lo1 = fminf(lo1, lo2);
+      hi1 = fmaxf(hi1, hi2);
+    }
+#pragma unroll
+    for (int o = TPR / 2; o > 0; o >>= 1) {
+      lo1 = fminf(lo1, __shfl_xor_sync(0xffffffffu, lo1, o));
+      hi1 = fmaxf(hi1, __shfl_xor_sync(0xffffffffu, hi1, o));
+      if constexpr (NG == 2) {
+        lo2 = fminf(lo2, __shfl_xor_sync(0xffffffffu, lo2, o));
+        hi2 = fmaxf(hi2, __shfl_xor_sync(0xffffffffu, hi2, o));
+      }
+    }
+    if (!live || isq) continue;
+    float s1, z1, inv1, s2, z2, inv2;
+    const uint32_t p1 = group_params<DT>(lo1, hi1, s1, z1, inv1);
+    uint32_t p2 = p1;
+    s2 = s1; z2 = z1; inv2 = inv1;
+    if constexpr (NG == 2) p2 = group_params<DT>(lo2, hi2, s2, z2, inv2);
+    const uint32_t w1 = encode8(x1, s1, z1, inv1), w2 = encode8(x2, s2, z2, inv2);
+    const int64_t blk = slot / a.block_size;
+    const int64_t crow = (blk * a.hkv + h) * a.block_size + (slot - blk * a.block_size);
+    uint32_t* cw = reinterpret_cast<uint32_t*>(isv ? a.vc : a.kc) + crow * (D / 8);
+    uint32_t* pw = (isv ? a.vp : a.kp) + crow * NG;
+    if constexpr (NG == 2) {
+      reinterpret_cast<uint2*>(cw)[j] = make_uint2(w1, w2);
+      if (j == 0) *reinterpret_cast<uint2*>(pw) = make_uint2(p1, p2);
+    } else {
+      cw[j] = w1;
+      cw[j + 4] = w2;
+      if (j == 0) *pw = p1;
+    }
+    uint4* held = isv ? a.v_out : a.k_out;
+    if (held) {
+      st_v4(held + vec, pack8<DT>(x1));
+      st_v4(held + vec + TPR, pack8<DT>(x2));
+    }
+  }
+}
+
+// Block copy: CTA (pair, part); a part is up to 1024 16-byte vectors of the pair's four runs.  Every thread
+// has its four loads in flight before the first store.
+constexpr int kCopyPart = 1024;
+__global__ void __launch_bounds__(256) copy_blocks_int4_kernel(const int32_t* __restrict__ pairs, int code_vecs,
+                                                               int param_vecs, int num_blocks, uint4* kc, uint4* vc,
+                                                               uint4* kp, uint4* vp) {
+  const int32_t src = __ldg(pairs + 2 * (int64_t)blockIdx.x), dst = __ldg(pairs + 2 * (int64_t)blockIdx.x + 1);
+  if (src < 0 || src >= num_blocks || dst < 0 || dst >= num_blocks) {
+    if (threadIdx.x == 0 && blockIdx.y == 0) PA_RECORD_ERROR(PA_ERRBIT_INDEX);
+    return;
+  }
+  const int total = 2 * (code_vecs + param_vecs);
+  for (int part = blockIdx.y * kCopyPart; part < total; part += gridDim.y * kCopyPart) {
+    uint4 u[kCopyPart / 256];
+    uint4* to[kCopyPart / 256];
+#pragma unroll
+    for (int e = 0; e < kCopyPart / 256; ++e) {
+      const int i = part + e * 256 + threadIdx.x;
+      to[e] = nullptr;
+      if (i < total) {
+        uint4* base;
+        int64_t per = code_vecs;
+        int o = i;
+        if (i < code_vecs) {
+          base = kc;
+        } else if (i < 2 * code_vecs) {
+          base = vc;
+          o = i - code_vecs;
+        } else {
+          per = param_vecs;
+          o = i - 2 * code_vecs;
+          base = kp;
+          if (o >= param_vecs) {
+            base = vp;
+            o -= param_vecs;
+          }
+        }
+        u[e] = ld_plain_v4(base + src * per + o);
+        to[e] = base + dst * per + o;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kCopyPart / 256; ++e)
+      if (to[e]) st_v4(to[e], u[e]);
+  }
+}
+
+// 8 codes of a word -> values s * (code + z), rounded to the type.
+template <int DT>
+__device__ __forceinline__ uint4 expand8(uint32_t w, uint32_t param) {
+  const float2 p = Elt<DT>::to_f2(param);
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(p.x, __fadd_rn((float)((w >> (4 * i)) & 15u), p.y));
+  return pack8<DT>(x);
+}
+
+// Expansion: CTA (pair and K or V, part of the block's rows); rows in the order of the 16-bit block.
+template <int DT, int D>
+__global__ void __launch_bounds__(256) load_blocks_int4_kernel(const int32_t* __restrict__ pairs, int hkv,
+                                                               int block_size, int num_blocks, int num_dst,
+                                                               const uint32_t* __restrict__ kc,
+                                                               const uint32_t* __restrict__ vc,
+                                                               const uint32_t* __restrict__ kp,
+                                                               const uint32_t* __restrict__ vp, uint4* __restrict__ k,
+                                                               uint4* __restrict__ v) {
+  constexpr int TPR = D / 16, NG = D / 64;
+  const int64_t pair = blockIdx.x >> 1;
+  const bool isv = blockIdx.x & 1;
+  const int32_t src = __ldg(pairs + 2 * pair), dst = __ldg(pairs + 2 * pair + 1);
+  if (src < 0 || src >= num_blocks || dst < 0 || dst >= num_dst) {
+    if (threadIdx.x == 0 && blockIdx.y == 0 && !isv) PA_RECORD_ERROR(PA_ERRBIT_INDEX);
+    return;
+  }
+  const int64_t rows = (int64_t)hkv * block_size;
+  const uint32_t* codes = (isv ? vc : kc) + src * rows * (D / 8);
+  const uint32_t* params = (isv ? vp : kp) + src * rows * NG;
+  uint4* out = (isv ? v : k) + dst * rows * (D / 8);
+  const int total = (int)rows * TPR;
+  for (int i = blockIdx.y * blockDim.x + threadIdx.x; i < total; i += gridDim.y * blockDim.x) {
+    const int row = i / TPR, j = i % TPR;     // row = token * hkv + head of the 16-bit block
+    const int tok = row / hkv, h = row - tok * hkv;
+    const int64_t crow = (int64_t)h * block_size + tok;
+    uint32_t w1, w2, p1, p2;
+    if constexpr (NG == 2) {
+      const uint2 w = __ldg(reinterpret_cast<const uint2*>(codes + crow * (D / 8)) + j);
+      const uint2 p = __ldg(reinterpret_cast<const uint2*>(params + crow * NG));
+      w1 = w.x; w2 = w.y; p1 = p.x; p2 = p.y;
+    } else {
+      w1 = __ldg(codes + crow * (D / 8) + j);
+      w2 = __ldg(codes + crow * (D / 8) + j + 4);
+      p1 = p2 = __ldg(params + crow);
+    }
+    uint4* o = out + (int64_t)row * (D / 8) + j;
+    st_v4(o, expand8<DT>(w1, p1));
+    st_v4(o + TPR, expand8<DT>(w2, p2));
+  }
+}
+
+int check_int4_cache(const void* kc, const void* vc, const void* kp, const void* vp, int num_blocks, int block_size,
+                     int num_kv_heads, int head_dim) {
+  if (!kc || !vc || !kp || !vp || num_blocks < 0 || num_kv_heads <= 0 || head_dim <= 0) return PA_ERR_INVALID;
+  if (!valid_block_size(block_size) || !valid_head_dim(head_dim)) return PA_ERR_UNSUPPORTED;
+  if ((int64_t)num_kv_heads * block_size * head_dim >= (1ll << 31)) return PA_ERR_UNSUPPORTED;  // 32-bit offsets in a block
+  if (!aligned16(kc) || !aligned16(vc) || !aligned16(kp) || !aligned16(vp)) return PA_ERR_ALIGN;
+  return PA_OK;
+}
+
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+
+template <bool ROPE>
+int launch_write(const WriteArgs& a, int head_dim, int dtype, cudaStream_t st) {
+  int64_t blocks = ((int64_t)a.total + 255) / 256;
+  const int64_t cap = (int64_t)sm_count() * 8;  // at most one resident wave: every CTA strides over the items
+  if (blocks > cap) blocks = cap;
+  auto kern = dtype == PA_BF16
+                  ? (head_dim == 128 ? write_kv_int4_kernel<PA_BF16, 128, ROPE> : write_kv_int4_kernel<PA_BF16, 64, ROPE>)
+                  : (head_dim == 128 ? write_kv_int4_kernel<PA_F16, 128, ROPE> : write_kv_int4_kernel<PA_F16, 64, ROPE>);
+  return launch_programmatic(kern, dim3((unsigned)blocks), dim3(256), 0, st, a);
+}
+
+}  // namespace
+
+extern "C" int pa_write_kv_int4(const void* k, const void* v, const int64_t* slot_mapping, int num_tokens,
+                                void* k_codes, void* v_codes, void* k_params, void* v_params, void* k_out,
+                                void* v_out, int num_blocks, int block_size, int num_kv_heads, int head_dim, int dtype,
+                                void* stream) {
+  int s = check_int4_cache(k_codes, v_codes, k_params, v_params, num_blocks, block_size, num_kv_heads, head_dim);
+  if (s != PA_OK) return s;
+  if (!valid_dtype(dtype)) return PA_ERR_UNSUPPORTED;
+  if (num_tokens < 0) return PA_ERR_INVALID;
+  if (num_tokens == 0) return PA_OK;
+  if (!k || !v || !slot_mapping) return PA_ERR_INVALID;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_out) || !aligned16(v_out) || !aligned8(slot_mapping))
+    return PA_ERR_ALIGN;
+  const int64_t total = (int64_t)num_tokens * 2 * num_kv_heads * (head_dim / 16);
+  if (total >= (1ll << 31) - 32) return PA_ERR_UNSUPPORTED;
+  WriteArgs a = {};
+  a.k = (const uint4*)k;
+  a.v = (const uint4*)v;
+  a.slots = slot_mapping;
+  a.kc = (uint8_t*)k_codes;
+  a.vc = (uint8_t*)v_codes;
+  a.kp = (uint32_t*)k_params;
+  a.vp = (uint32_t*)v_params;
+  a.k_out = (uint4*)k_out;
+  a.v_out = (uint4*)v_out;
+  a.num_slots = (int64_t)num_blocks * block_size;
+  a.total = (int)total;
+  a.hkv = num_kv_heads;
+  a.block_size = block_size;
+  return launch_write<false>(a, head_dim, dtype, (cudaStream_t)stream);
+}
+
+extern "C" int pa_rope_write_kv_int4(const void* q, void* q_out, const void* k, const void* v,
+                                     const int64_t* positions, const float* cos_table, const float* sin_table,
+                                     int max_position, const int64_t* slot_mapping, int num_tokens, int num_q_heads,
+                                     void* k_codes, void* v_codes, void* k_params, void* v_params, void* k_out,
+                                     void* v_out, int num_blocks, int block_size, int num_kv_heads, int head_dim,
+                                     int dtype, void* stream) {
+  if (num_tokens < 0 || num_q_heads <= 0 || max_position <= 0) return PA_ERR_INVALID;
+  int s = check_int4_cache(k_codes, v_codes, k_params, v_params, num_blocks, block_size, num_kv_heads, head_dim);
+  if (s != PA_OK) return s;
+  if (!valid_dtype(dtype)) return PA_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return PA_OK;
+  if (!q || !q_out || !k || !v || !positions || !cos_table || !sin_table || !slot_mapping) return PA_ERR_INVALID;
+  if (!aligned16(q) || !aligned16(q_out) || !aligned16(k) || !aligned16(v) || !aligned16(k_out) ||
+      !aligned16(v_out) || !aligned16(cos_table) || !aligned16(sin_table) || !aligned8(positions) ||
+      !aligned8(slot_mapping))
+    return PA_ERR_ALIGN;
+  const int64_t total = (int64_t)num_tokens * ((int64_t)num_q_heads + 2ll * num_kv_heads) * (head_dim / 16);
+  if (total >= (1ll << 31) - 32) return PA_ERR_UNSUPPORTED;
+  WriteArgs a = {};
+  a.q = (const uint4*)q;
+  a.q_out = (uint4*)q_out;
+  a.k = (const uint4*)k;
+  a.v = (const uint4*)v;
+  a.positions = positions;
+  a.cos_t = (const float4*)cos_table;
+  a.sin_t = (const float4*)sin_table;
+  a.slots = slot_mapping;
+  a.kc = (uint8_t*)k_codes;
+  a.vc = (uint8_t*)v_codes;
+  a.kp = (uint32_t*)k_params;
+  a.vp = (uint32_t*)v_params;
+  a.k_out = (uint4*)k_out;
+  a.v_out = (uint4*)v_out;
+  a.num_slots = (int64_t)num_blocks * block_size;
+  a.max_position = max_position;
+  a.total = (int)total;
+  a.hq = num_q_heads;
+  a.hkv = num_kv_heads;
+  a.block_size = block_size;
+  return launch_write<true>(a, head_dim, dtype, (cudaStream_t)stream);
+}
+
+extern "C" int pa_copy_blocks_int4(const int32_t* pairs, int num_pairs, void* k_codes, void* v_codes, void* k_params,
+                                   void* v_params, int num_blocks, int block_size, int num_kv_heads, int head_dim,
+                                   void* stream) {
+  int s = check_int4_cache(k_codes, v_codes, k_params, v_params, num_blocks, block_size, num_kv_heads, head_dim);
+  if (s != PA_OK) return s;
+  if (num_pairs < 0) return PA_ERR_INVALID;
+  if (num_pairs == 0) return PA_OK;
+  if (!pairs) return PA_ERR_INVALID;
+  if (reinterpret_cast<uintptr_t>(pairs) & 3u) return PA_ERR_ALIGN;
+  const int rows = num_kv_heads * block_size;
+  const int code_vecs = rows * (head_dim / 32), param_vecs = rows * (head_dim / 64) / 4;
+  const int parts = (2 * (code_vecs + param_vecs) + kCopyPart - 1) / kCopyPart;
+  const dim3 grid((unsigned)num_pairs, (unsigned)(parts > 65535 ? 65535 : parts));
+  copy_blocks_int4_kernel<<<grid, 256, 0, (cudaStream_t)stream>>>(pairs, code_vecs, param_vecs, num_blocks,
+                                                                  (uint4*)k_codes, (uint4*)v_codes, (uint4*)k_params,
+                                                                  (uint4*)v_params);
+  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+extern "C" int pa_load_blocks_int4(const int32_t* pairs, int num_pairs, const void* k_codes, const void* v_codes,
+                                   const void* k_params, const void* v_params, int num_blocks, void* k_cache,
+                                   void* v_cache, int num_dst_blocks, int block_size, int num_kv_heads, int head_dim,
+                                   int dtype, void* stream) {
+  int s = check_int4_cache(k_codes, v_codes, k_params, v_params, num_blocks, block_size, num_kv_heads, head_dim);
+  if (s != PA_OK) return s;
+  if (!valid_dtype(dtype)) return PA_ERR_UNSUPPORTED;
+  if (!k_cache || !v_cache || num_dst_blocks < 0 || num_pairs < 0) return PA_ERR_INVALID;
+  if (!aligned16(k_cache) || !aligned16(v_cache)) return PA_ERR_ALIGN;
+  if (num_pairs == 0) return PA_OK;
+  if (!pairs || num_pairs >= (1 << 30)) return PA_ERR_INVALID;
+  if (reinterpret_cast<uintptr_t>(pairs) & 3u) return PA_ERR_ALIGN;
+  const int64_t total = (int64_t)num_kv_heads * block_size * (head_dim / 16);
+  const int64_t parts = (total + 1023) / 1024;  // four items a thread
+  auto kern = dtype == PA_BF16 ? (head_dim == 128 ? load_blocks_int4_kernel<PA_BF16, 128> : load_blocks_int4_kernel<PA_BF16, 64>)
+                               : (head_dim == 128 ? load_blocks_int4_kernel<PA_F16, 128> : load_blocks_int4_kernel<PA_F16, 64>);
+  const dim3 grid((unsigned)num_pairs * 2u, (unsigned)(parts > 65535 ? 65535 : parts));
+  kern<<<grid, 256, 0, (cudaStream_t)stream>>>(pairs, num_kv_heads, block_size, num_blocks, num_dst_blocks,
+                                               (const uint32_t*)k_codes, (const uint32_t*)v_codes,
+                                               (const uint32_t*)k_params, (const uint32_t*)v_params, (uint4*)k_cache,
+                                               (uint4*)v_cache);
+  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
