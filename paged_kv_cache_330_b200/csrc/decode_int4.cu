@@ -2,10 +2,37 @@
 //
 // For every sequence b and query head h,
 //   out[b][h] = sum_t softmax_t(scale <q[b][h], Kd_b[t][h/G]>) Vd_b[t][h/G],
-// with Kd, Vd the rows s * (code + z).  One CTA per (sequence, KV head); 128
-// tokens a round: thread = token for the scores, thread = column for PV.
+// with Kd, Vd the rows s * (code + z).  A row of D 128 is 72 bytes (64 of codes, 8 of parameters): 16-bit caches
+// hold 256.  At that size the work per byte, not HBM, is what has to be kept small, so the kernel is built
+// around warps that never wait for one another.
+//
+// Work split.  A segment is one (sequence, KV head), cut into tiles of 32 tokens; all segments end to end form
+// one line of T tiles.  CTA c takes tiles [T c / n, T (c+1) / n), its warps equal parts of that.  Every warp
+// walks its own part: it looks its blocks up, brings its tiles in with bulk copies into a ring of its own
+// (one mbarrier per stage, no other warp involved) and keeps the softmax state and the output of the current
+// segment in registers.  What a warp holds of a segment is a piece: a whole segment is written out at once, a
+// partial one goes to shared memory, and after the one barrier at the end of the CTA the pieces of a segment
+// are joined, first within the CTA, then, for the at most two segments that a CTA shares with its neighbours,
+// through the workspace by the CTA that finishes last (a counter per head, no waiting).  The joining order is
+// the order of the line, so results do not depend on timing.
+//
+// Mathematics.  Products run on mma.m16n8k16 (fp16 in, fp32 out) with tokens (scores) or columns (PV) as the 16
+// rows and up to 8 heads of the group as the 8 columns; G 16 takes two column tiles.
+//   * Codes enter as fp16 subnormals: a nibble in the low four bits of a half is code * 2^-24, in the next four
+//     code * 2^-20, exactly.  Widening a word of 8 codes is one shift and four ANDs, with no offset to take out
+//     again; the factors 2^24 and 16 sit in the score scale, in q (its odd values enter divided by 16) and in
+//     the final scaling of the output rows.
+//   * Scores: s_t = sum_group s_K (sum code q + z_K sum q); the group sums of q come from a product with codes 1.
+//   * PV: the weight of a token enters times its V scale, P' = 2^(x - R) s_V in fp16 (rounded once, 2^-11; its
+//     rounded value also multiplies the zero point, so code and zero-point parts carry the same rounding and
+//     the error stays relative to the value, not to the code):  O += P' code,  Z += P' z_V (fp32).
+//   * Online softmax with a reference R per head that moves only when it must: R is set from a piece's first
+//     tile so that its largest P' lies in (2^3, 2^4], and is raised only when some P' reaches 2^15 or the sum l
+//     passes 2^100.  Any R gives the same quotient O / l; the usual tile needs no maximum, no shuffles and no
+//     rescaling of O, one vote tells.  l and O are fp32.
 
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "host_common.h"
@@ -16,109 +43,876 @@ namespace {
 
 using namespace pa;
 
+constexpr int kTile = 32;            // tokens per tile: two 16-token chunks, each within one block
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kUnit = 16777216.f;  // 2^24: what a code's fp16 subnormal stands for, inverted
+
 struct Params {
   const void* q;
   void* out;
   float* lse;
-  const uint8_t* kc;
-  const uint8_t* vc;
-  const uint32_t* kp;
-  const uint32_t* vp;
+  const uint8_t* base[4];  // K codes, V codes, K parameters, V parameters
   const int32_t* block_tables;
   const int32_t* context_lens;
+  int* ws_cnt;   // [batch * Hq] CTAs that have added their share of a head (zero between calls)
+  float* ws_r;   // [slots][G] reference R of a share
+  float* ws_l;   // [slots][G]
+  float* ws_o;   // [slots][G][D]
   int max_blocks_per_seq, batch, num_q_heads, num_kv_heads, block_size, num_blocks;
   float scale_log2;
 };
 
-template <int DT, int D>
-__global__ void __launch_bounds__(128) decode_int4_kernel(const Params p, int G) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  constexpr int NG = D / 64;
-  __shared__ float qs[16 * D], ps[128 * 16], red[4][16];
-  __shared__ int64_t rows[128];
-  const int b = blockIdx.y, g = blockIdx.x, tid = threadIdx.x, warp = tid >> 5;
-  const int cap = p.max_blocks_per_seq * p.block_size;
-  int L = __ldg(p.context_lens + b);
-  if (L < 0 || L > cap) {
-    if (tid == 0) PA_RECORD_ERROR(PA_ERRBIT_INDEX);
-    L = min(max(L, 0), cap);
-  }
-  using T = typename Elt<DT>::T;
-  const T* q = reinterpret_cast<const T*>(p.q) + ((size_t)b * p.num_q_heads + (size_t)g * G) * D;
-  for (int i = tid; i < G * D; i += 128) qs[i] = (float)q[i] * p.scale_log2;
-  float m[16], l[16], o[16];
-  for (int h = 0; h < 16; ++h) m[h] = -INFINITY, l[h] = 0.f, o[h] = 0.f;
-  for (int t0 = 0; t0 < L; t0 += 128) {
-    __syncthreads();
-    const int t = t0 + tid;
-    float s[16];
-    for (int h = 0; h < 16; ++h) s[h] = -INFINITY;
-    if (t < L) {
-      int blk = __ldg(p.block_tables + (size_t)b * p.max_blocks_per_seq + t / p.block_size);
-      if (blk < 0 || blk >= p.num_blocks) {
-        PA_RECORD_ERROR(PA_ERRBIT_INDEX);
-        blk = 0;
+enum : int { F_FIRST = 1, F_LAST = 2, F_HEAD = 4, F_TAIL = 8, F_VALID = 16 };
+
+// A partial piece as the joining step sees it: its segment, whether it holds the segment's first (F_HEAD) and
+// last (F_TAIL) tile, the segment's tiles and where they start on the line.
+struct Piece {
+  int b, g, flags, nt;
+  long long seg_start;
+};
+
+template <int D, int G, int NW, int NS>
+struct Layout {
+  static constexpr int NG = D / 64, ROWB = D / 2, PARB = NG * 4;
+  static constexpr int K_OFF = 0, V_OFF = kTile * ROWB, KP_OFF = 2 * kTile * ROWB, VP_OFF = KP_OFF + kTile * PARB;
+  static constexpr int STAGE = VP_OFF + kTile * PARB;
+  static constexpr int PART = (G * (D + 2) * 4 + 15) / 16 * 16;  // a partial piece: o [G][D], R [G], l [G]
+  static constexpr int RING = NS * STAGE > PART ? NS * STAGE : (PART + 127) / 128 * 128;  // also the last piece
+  static constexpr int RING_OFF = 0;
+  static constexpr int PART_OFF = RING_OFF + NW * RING;          // the first piece of every warp
+  static constexpr int PIECE_OFF = (PART_OFF + NW * PART + 15) / 16 * 16;  // Piece [NW][2]
+  static constexpr int DESC_OFF = PIECE_OFF + NW * 2 * (int)sizeof(Piece);  // int4 [NW][NS]
+  static constexpr int BAR_OFF = DESC_OFF + NW * NS * 16;        // full [NW][NS]
+  static constexpr int START_OFF = BAR_OFF + NW * NS * 8;        // Start [NW]: where each warp begins
+  static constexpr int SCAN_OFF = START_OFF + NW * 16;           // int64 [NW]
+  static constexpr int BYTES = SCAN_OFF + NW * 8;
+  static_assert(STAGE % 128 == 0 && sizeof(Piece) % 8 == 0 && PIECE_OFF % 8 == 0, "alignment");
+};
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+  return d;
+}
+__device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t trans8x8(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_h2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t hmax2_bits(uint32_t a, uint32_t b) {
+  const __half2 h = __hmax2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ float rows_max(float v) {  // over the 8 lanes that share a column
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+__device__ __forceinline__ float rows_sum(float v) {
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;  // a nibble of each half, worth 2^-24 and 2^-20
+
+// ------------------------------------------------------------------ a warp's state over one piece
+template <int DT, int D, int G>
+struct State {
+  static constexpr int NG = D / 64, KS = D / 16, NT = (G + 7) / 8, WPL = D / 32;  // WPL: K words a lane reads of a row
+  uint32_t qb[NT][KS][2];  // q as B operand (fp16, prescaled; odd values divided by 16)
+  float qsum[NT][NG][2];   // sum of q over a group times 2^-24, heads 8nt + 2c + {0,1}
+  float o[NT][KS][4];      // O^T times 2^-24 (rows g) and 2^-20 (rows g + 8), columns heads
+  float z[NT][NG][2];      // this lane's part of sum P' z_V
+  float l[NT][2];          // this lane's part of sum 2^(x - R)
+  float R[NT][2];
+  float qs;                // scale * log2(e) * 2^24 / prescale
+  bool fresh;              // some head has met no non-zero V scale yet: its R is not set
+
+  // qrows: the group's [G][D] rows of q.  A lane loads just the values its operands hold.
+  __device__ __forceinline__ void begin(const uint8_t* qrows, float scale_log2, int lane) {
+    const int g = lane >> 2, c = lane & 3;
+    uint4 raw[NT][WPL];
+    float amax = 0.f;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < WPL; ++i) {
+        // stored word WPL * c + i of a row: 8 values from `base` on
+        const int base = D == 128 ? 64 * (i & 1) + 8 * (2 * c + (i >> 1)) : 8 * (2 * c + i);
+        raw[nt][i] = make_uint4(0, 0, 0, 0);
+        if (nt * 8 + g < G) raw[nt][i] = __ldcg(reinterpret_cast<const uint4*>(qrows + ((nt * 8 + g) * D + base) * 2));
       }
-      const int64_t row = ((int64_t)blk * p.num_kv_heads + g) * p.block_size + t % p.block_size;
-      rows[tid] = row;
-      for (int h = 0; h < G; ++h) s[h] = 0.f;
-      const uint32_t* w = reinterpret_cast<const uint32_t*>(p.kc) + row * (D / 8);
-      for (int j = 0; j < D / 8; ++j) {
-        const float2 par = Elt<DT>::to_f2(__ldg(p.kp + row * NG + j % NG));
-        const uint32_t word = __ldg(w + j);
-        const int d = 64 * (j % NG) + 8 * (j / NG);
-        for (int e = 0; e < 8; ++e) {
-          const float x = par.x * ((float)((word >> (4 * e)) & 15u) + par.y);
-          for (int h = 0; h < G; ++h) s[h] = fmaf(x, qs[h * D + d + e], s[h]);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < WPL; ++i) {
+        const uint32_t w[4] = {raw[nt][i].x, raw[nt][i].y, raw[nt][i].z, raw[nt][i].w};
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const float2 f = Elt<DT>::to_f2(w[m]);
+          amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+      }
+    amax = warp_max(amax);
+    int e = 0;
+    if (amax > 0.f) {
+      int k;
+      frexpf(amax, &k);  // amax in [2^(k-1), 2^k)
+      e = min(60, max(-60, 15 - k));
+    }
+    const float f = __int_as_float((127 + e) << 23), finv = __int_as_float((127 - e) << 23);
+    qs = scale_log2 * finv * kUnit;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < WPL; ++i) {
+        const uint32_t w[4] = {raw[nt][i].x, raw[nt][i].y, raw[nt][i].z, raw[nt][i].w};
+        float x[8];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const float2 v = Elt<DT>::to_f2(w[m]);
+          x[2 * m] = v.x * f;
+          x[2 * m + 1] = v.y * f * 0.0625f;
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          qb[nt][2 * i + s][0] = pack_h2(x[2 * s], x[2 * s + 4]);
+          qb[nt][2 * i + s][1] = pack_h2(x[2 * s + 1], x[2 * s + 5]);
+        }
+      }
+#pragma unroll
+      for (int grp = 0; grp < NG; ++grp) {
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = grp; i < WPL; i += NG)
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+            mma_f16(acc, 0x00010001u, 0x00010001u, 0x00100010u, 0x00100010u, qb[nt][2 * i + s][0], qb[nt][2 * i + s][1]);
+        qsum[nt][grp][0] = acc[0];
+        qsum[nt][grp][1] = acc[1];
+        z[nt][grp][0] = z[nt][grp][1] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < KS; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
+      l[nt][0] = l[nt][1] = R[nt][0] = R[nt][1] = 0.f;
+    }
+    fresh = true;
+  }
+
+  // Moves the references of the heads that need it, so that the tile's scores x (relative to R; -inf where
+  // masked) give P' <= 2^4 and l <= 2^91.  svm: the larger V scale of each of this lane's rows.
+  __device__ __forceinline__ void rebase(float (&x)[2][NT][4], const float (&svm)[4]) {
+    bool still = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float u = -INFINITY, v = l[nt][e] > 0.f ? __log2f(l[nt][e]) : -INFINITY;
+        bool set = false;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float xr = x[r >> 1][nt][2 * (r & 1) + e];
+          v = fmaxf(v, xr);
+          u = fmaxf(u, svm[r] > 0.f ? xr + __log2f(svm[r]) : -INFINITY);
+        }
+#pragma unroll
+        for (int i = 0; i < KS; ++i) set |= o[nt][i][e] != 0.f || o[nt][i][2 + e] != 0.f;
+#pragma unroll
+        for (int grp = 0; grp < NG; ++grp) set |= z[nt][grp][e] != 0.f;
+        // every lane of a column has to agree on whether its O is still all zero
+        float any = set ? 1.f : 0.f;
+        u = rows_max(u);
+        v = rows_max(v);
+        set = rows_max(any) > 0.f;
+        float up = fmaxf(u - 4.f, v - 90.f);
+        if (set) up = fmaxf(up, 0.f);
+        else if (u == -INFINITY) up = v, still = true;
+        up = ceilf(up);
+        if (!(fabsf(up) < 1e30f)) up = 0.f;  // not-a-number inputs: leave the references alone
+        const float f = exp2f(-up);
+        if (l[nt][e] > 0.f) l[nt][e] *= f;
+        if (set) {
+#pragma unroll
+          for (int i = 0; i < KS; ++i) o[nt][i][e] *= f, o[nt][i][2 + e] *= f;
+#pragma unroll
+          for (int grp = 0; grp < NG; ++grp) z[nt][grp][e] *= f;
+        }
+        R[nt][e] += up;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[r >> 1][nt][2 * (r & 1) + e] -= up;
+      }
+    fresh = __any_sync(0xffffffffu, still);
+  }
+
+  // One tile at shared address `st` (a stage), nv of its 32 tokens valid.
+  template <typename LY>
+  __device__ __forceinline__ void tile(uint32_t st, int nv, int lane) {
+    const int g = lane >> 2, c = lane & 3;
+    // ---- scores: rows tokens g, g + 8, g + 16, g + 24 (r = 2 mt + hh), columns heads 8nt + 2c + {0,1}
+    float x[2][NT][4];
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+      const uint32_t ra = st + LY::K_OFF + (16 * mt + g) * LY::ROWB + 4 * WPL * c, rb = ra + 8 * LY::ROWB;
+      uint32_t wa[WPL], wb[WPL];
+      if constexpr (WPL == 4) {
+        const uint4 a = lds128(ra), b = lds128(rb);
+        wa[0] = a.x; wa[1] = a.y; wa[2] = a.z; wa[3] = a.w;
+        wb[0] = b.x; wb[1] = b.y; wb[2] = b.z; wb[3] = b.w;
+      } else {
+        const uint2 a = lds64(ra), b = lds64(rb);
+        wa[0] = a.x; wa[1] = a.y;
+        wb[0] = b.x; wb[1] = b.y;
+      }
+      float acc[NT][NG][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int grp = 0; grp < NG; ++grp) acc[nt][grp][0] = acc[nt][grp][1] = acc[nt][grp][2] = acc[nt][grp][3] = 0.f;
+#pragma unroll
+      for (int i = 0; i < WPL; ++i)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const uint32_t a = wa[i] >> (8 * s), b = wb[i] >> (8 * s);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma_f16(acc[nt][i % NG], a & kLow, b & kLow, a & kHigh, b & kHigh, qb[nt][2 * i + s][0],
+                    qb[nt][2 * i + s][1]);
+        }
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        const uint32_t pa = st + LY::KP_OFF + (16 * mt + 8 * hh + g) * LY::PARB;
+        float2 par[NG];
+        if constexpr (NG == 2) {
+          const uint2 w = lds64(pa);
+          par[0] = Elt<DT>::to_f2(w.x);
+          par[1] = Elt<DT>::to_f2(w.y);
+        } else {
+          par[0] = Elt<DT>::to_f2(lds32(pa));
+        }
+#pragma unroll
+        for (int grp = 0; grp < NG; ++grp) {
+          const float sq = par[grp].x * qs;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              x[mt][nt][2 * hh + e] = fmaf(fmaf(par[grp].y, qsum[nt][grp][e], acc[nt][grp][2 * hh + e]), sq,
+                                           grp == 0 ? -R[nt][e] : x[mt][nt][2 * hh + e]);
         }
       }
     }
-    float mn[16];
-    for (int h = 0; h < G; ++h) {
-      float v = s[h];
-      for (int k = 16; k > 0; k >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, k));
-      if ((tid & 31) == 0) red[warp][h] = v;
-    }
-    __syncthreads();
-    for (int h = 0; h < G; ++h) {
-      mn[h] = fmaxf(m[h], fmaxf(fmaxf(red[0][h], red[1][h]), fmaxf(red[2][h], red[3][h])));
-      ps[tid * 16 + h] = fast_exp2(s[h] - mn[h]);
-      const float alpha = fast_exp2(m[h] - mn[h]);
-      l[h] *= alpha;
-      o[h] *= alpha;
-      m[h] = mn[h];
-    }
-    __syncthreads();
-    const int n = min(128, L - t0), d = tid;
-    for (int k = 0; k < n; ++k) {
-      float x = 0.f;
-      if (d < D) {
-        const int64_t row = rows[k];
-        const int grp = d / 64, word = (d % 64) / 8 * NG + grp;
-        const uint32_t c = (__ldg(reinterpret_cast<const uint32_t*>(p.vc) + row * (D / 8) + word) >> (4 * (d % 8))) & 15u;
-        const float2 par = Elt<DT>::to_f2(__ldg(p.vp + row * NG + grp));
-        x = par.x * ((float)c + par.y);
+    // ---- V parameters of the same rows
+    float sv[4][NG], zv[4][NG];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const uint32_t pa = st + LY::VP_OFF + (8 * r + g) * LY::PARB;
+      uint32_t w[NG];
+      if constexpr (NG == 2) {
+        const uint2 u = lds64(pa);
+        w[0] = u.x;
+        w[1] = u.y;
+      } else {
+        w[0] = lds32(pa);
       }
-      for (int h = 0; h < G; ++h) {
-        o[h] = fmaf(ps[k * 16 + h], x, o[h]);
-        l[h] += ps[k * 16 + h];
+#pragma unroll
+      for (int grp = 0; grp < NG; ++grp) {
+        const float2 f = Elt<DT>::to_f2(w[grp]);
+        sv[r][grp] = f.x;
+        zv[r][grp] = f.y;
       }
+    }
+    if (nv < kTile) {  // rows past the end hold anything, NaN among it
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (8 * r + g >= nv) {
+#pragma unroll
+          for (int grp = 0; grp < NG; ++grp) sv[r][grp] = zv[r][grp] = 0.f;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) x[r >> 1][nt][2 * (r & 1)] = x[r >> 1][nt][2 * (r & 1) + 1] = -INFINITY;
+        }
+    }
+    // ---- weights; taken again after a move of the references
+    uint32_t pk[NT][NG][4];
+    float sum[NT][2];
+    auto weights = [&]() -> bool {
+      uint32_t big = 0;
+      bool over = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        sum[nt][0] = l[nt][0];
+        sum[nt][1] = l[nt][1];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float p0 = fast_exp2(x[r >> 1][nt][2 * (r & 1)]), p1 = fast_exp2(x[r >> 1][nt][2 * (r & 1) + 1]);
+          sum[nt][0] += p0;
+          sum[nt][1] += p1;
+#pragma unroll
+          for (int grp = 0; grp < NG; ++grp) {
+            pk[nt][grp][r] = pack_h2(p0 * sv[r][grp], p1 * sv[r][grp]);
+            big = hmax2_bits(big, pk[nt][grp][r]);
+          }
+        }
+        over |= !(sum[nt][0] < 1.2676506e30f) || !(sum[nt][1] < 1.2676506e30f);  // 2^100
+      }
+      return over || ((big + 0x08000800u) & 0x80008000u) != 0;  // some P' of 2^15 or more
+    };
+    if (__any_sync(0xffffffffu, weights() || fresh)) {
+      float svm[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) svm[r] = NG == 2 ? fmaxf(sv[r][0], sv[r][NG - 1]) : sv[r][0];
+      rebase(x, svm);
+      weights();
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      l[nt][0] = sum[nt][0];
+      l[nt][1] = sum[nt][1];
+#pragma unroll
+      for (int grp = 0; grp < NG; ++grp)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&pk[nt][grp][r]));
+          z[nt][grp][0] = fmaf(p.x, zv[r][grp], z[nt][grp][0]);
+          z[nt][grp][1] = fmaf(p.y, zv[r][grp], z[nt][grp][1]);
+          pk[nt][grp][r] = trans8x8(pk[nt][grp][r]);  // tokens along the rows of the B operand
+        }
+    }
+    // ---- O^T += V^T P'^T: tokens 2c, 2c + 1, 2c + 8, 2c + 9 of each half; word `grp` of lane g's piece of a row holds
+    // values 64 grp + 8 g ..
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+      uint32_t w[4][NG];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const uint32_t a = st + LY::V_OFF + (16 * mt + 2 * c + (t & 1) + 8 * (t >> 1)) * LY::ROWB + 4 * NG * g;
+        if constexpr (NG == 2) {
+          const uint2 u = lds64(a);
+          w[t][0] = u.x;
+          w[t][1] = u.y;
+        } else {
+          w[t][0] = lds32(a);
+        }
+      }
+#pragma unroll
+      for (int grp = 0; grp < NG; ++grp)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const uint32_t sel = half ? 0x7632u : 0x5410u;
+          const uint32_t a = prmt(w[0][grp], w[1][grp], sel), b = prmt(w[2][grp], w[3][grp], sel);
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            const uint32_t as = a >> (8 * s), bs = b >> (8 * s);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_f16(o[nt][4 * grp + 2 * half + s], as & kLow, as & kHigh, bs & kLow, bs & kHigh,
+                      pk[nt][grp][2 * mt], pk[nt][grp][2 * mt + 1]);
+          }
+        }
     }
   }
-  T* out = reinterpret_cast<T*>(p.out) + ((size_t)b * p.num_q_heads + (size_t)g * G) * D;
-  for (int h = 0; h < G; ++h) {
-    if (tid < D) out[h * D + tid] = Elt<DT>::from_f(L > 0 ? o[h] / l[h] : 0.f);
-    if (tid == 0 && p.lse)
-      p.lse[(size_t)b * p.num_q_heads + g * G + h] = L > 0 ? (m[h] + __log2f(l[h])) * 0.6931471805599453f : -INFINITY;
+
+  // Completes the lanes' parts; after it l is the sum and z the zero-point part for every lane of a column.
+  __device__ __forceinline__ void finish() {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[nt][e] = rows_sum(l[nt][e]);
+#pragma unroll
+        for (int grp = 0; grp < NG; ++grp) z[nt][grp][e] = rows_sum(z[nt][grp][e]);
+      }
+  }
+  // The 8 output values 64 grp + 8 g .. of head 8nt + 2c + e, relative to R.
+  __device__ __forceinline__ void values(int nt, int grp, int e, float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = fmaf(o[nt][4 * grp + i][e], kUnit, z[nt][grp][e]);
+      v[2 * i + 1] = fmaf(o[nt][4 * grp + i][2 + e], kUnit / 16.f, z[nt][grp][e]);
+    }
+  }
+};
+
+// ------------------------------------------------------------------ kernel
+template <int DT, int D, int G, int NW, int NS>
+__global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p) {
+  using LY = Layout<D, G, NW, NS>;
+  using S = State<DT, D, G>;
+  using T = typename Elt<DT>::T;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + LY::BAR_OFF) + warp * NS;
+  struct Start {
+    long long pre;  // tiles of all sequences before b, per KV head
+    int b;
+  };
+  Start* starts = reinterpret_cast<Start*>(smem + LY::START_OFF);
+  long long* scan = reinterpret_cast<long long*>(smem + LY::SCAN_OFF);
+  Piece* pieces = reinterpret_cast<Piece*>(smem + LY::PIECE_OFF);
+  const int B = p.batch, Hkv = p.num_kv_heads, bs = p.block_size;
+  const int cap = p.max_blocks_per_seq * bs;
+
+  if (lane == 0) {
+    for (int i = 0; i < NS; ++i) mbar_init(&full[i], 1);
+    fence_mbar_init();
+    pieces[2 * warp].flags = pieces[2 * warp + 1].flags = 0;
+  }
+
+  // ---- the line: thread i counts the tiles of sequences [i * per, (i + 1) * per); a scan over the threads
+  const int per = (B + NW * 32 - 1) / (NW * 32);
+  const int i0 = min(B, (int)threadIdx.x * per), i1 = min(B, i0 + per);
+  auto len_of = [&](int i) { return min(max(__ldg(p.context_lens + i), 0), cap); };
+  long long mine = 0;
+  bool clamped = false;
+  for (int i = i0; i < i1; ++i) {
+    const int L = __ldg(p.context_lens + i);
+    clamped |= L < 0 || L > cap;
+    mine += (min(max(L, 0), cap) + kTile - 1) / kTile;
+  }
+  if (clamped && cta == 0) PA_RECORD_ERROR(PA_ERRBIT_INDEX);
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += t;
+  }
+  if (lane == 31) scan[warp] = incl;
+  __syncthreads();
+  long long before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    if (w < warp) before += scan[w];
+    total += scan[w];
+  }
+  total *= Hkv;
+  const long long ctas = min((long long)gridDim.x, total);  // at least one tile for each CTA that takes part
+  long long x0 = 0, n = 0;
+  if (cta < ctas) {
+    x0 = total * cta / ctas;
+    n = total * (cta + 1) / ctas - x0;
+  }
+  const long long lo = (before + incl - mine) * Hkv, hi = (before + incl) * Hkv;
+  for (int w = 0; w < NW; ++w) {
+    const long long x = x0 + n * w / NW;
+    if (x < lo || x >= hi) continue;
+    long long pre = before + incl - mine;
+    int i = i0;
+    for (; i < i1; ++i) {
+      const int nt = (len_of(i) + kTile - 1) / kTile;
+      if (x < (pre + nt) * Hkv) break;
+      pre += nt;
+    }
+    starts[w].b = i;
+    starts[w].pre = pre;
+  }
+  __syncthreads();
+
+  // ---- this warp's walk
+  const long long xs = x0 + n * warp / NW;
+  const int tiles = (int)(x0 + n * (warp + 1) / NW - xs);
+  int wb = 0, wg = 0, wL = 0, wnt = 1, wt = 0, left = tiles;  // the next tile to bring in
+  long long wseg = 0;                                         // where its segment starts on the line
+  int win_b = 0, win_len = 0, win_base = 0, win_phys = 0;     // windows of lengths and of block-table entries
+  bool piece_start = true, new_window = true;
+  if (tiles > 0) {
+    wb = starts[warp].b;
+    win_b = wb;
+    win_len = wb + lane < B ? len_of(wb + lane) : 0;
+    wL = __shfl_sync(0xffffffffu, win_len, 0);
+    wnt = (wL + kTile - 1) / kTile;
+    const long long in_seq = xs - starts[warp].pre * Hkv;
+    wg = (int)(in_seq / wnt);
+    wt = (int)(in_seq - (long long)wg * wnt);
+    wseg = xs - wt;
+  }
+  const uint32_t ring = smem_u32(smem + LY::RING_OFF) + warp * LY::RING;
+  int4* desc = reinterpret_cast<int4*>(smem + LY::DESC_OFF) + warp * NS;
+  const int bs_shift = __ffs(bs) - 1;
+  const int kind = lane & 3;  // what this lane copies of chunk lane / 4 of a tile (lanes 0 .. 7)
+  const uint32_t rowb = kind < 2 ? LY::ROWB : LY::PARB;
+  const uint8_t* kind_base = p.base[kind];
+  const uint32_t kind_off = kind == 0 ? LY::K_OFF : (kind == 1 ? LY::V_OFF : (kind == 2 ? LY::KP_OFF : LY::VP_OFF));
+
+  auto look_up = [&]() {  // block-table entries of the next 32 chunks of the walk's sequence
+    win_base = 2 * wt;
+    const int tok = (win_base + lane) * 16;
+    win_phys = tok < wL ? __ldg(p.block_tables + (size_t)wb * p.max_blocks_per_seq + (tok >> bs_shift)) : 0;
+    new_window = false;
+  };
+  auto bring = [&](int s) {  // the walk's next tile into stage s
+    if (new_window || 2 * wt - win_base >= 32 || 2 * wt < win_base) look_up();
+    const int nv = min(kTile, wL - wt * kTile), chunks = nv > 16 ? 2 : 1;
+    const int flags = (piece_start ? F_FIRST : 0) | (wt == wnt - 1 || left == 1 ? F_LAST : 0) |
+                      (wt == 0 ? F_HEAD : 0) | (wt == wnt - 1 ? F_TAIL : 0);
+    if (lane == 0) {
+      desc[s] = make_int4(wb, wg, nv | flags << 8, wnt);
+      mbar_arrive_expect_tx(&full[s], chunks * 16 * 2 * (LY::ROWB + LY::PARB));
+    }
+    int phys = __shfl_sync(0xffffffffu, win_phys, (2 * wt - win_base + (lane >> 2)) & 31);
+    __syncwarp();
+    const uint32_t stage = ring + s * LY::STAGE;
+    if (lane < 4 * chunks) {
+      if (phys < 0 || phys >= p.num_blocks) {  // broken caller invariant: record, read block 0 instead
+        PA_RECORD_ERROR(PA_ERRBIT_INDEX);
+        phys = 0;
+      }
+      const int tok = wt * kTile + (lane >> 2) * 16;
+      const size_t row = ((size_t)phys * Hkv + wg) * bs + (tok & (bs - 1));
+      bulk_load(stage + kind_off + (lane >> 2) * 16 * rowb, kind_base + row * rowb, 16 * rowb, &full[s]);
+    }
+    // step on
+    --left;
+    piece_start = false;
+    if (++wt == wnt && left > 0) {
+      piece_start = true;
+      wseg += wnt;
+      wt = 0;
+      if (++wg == Hkv) {
+        wg = 0;
+        new_window = true;
+        do {  // sequences without tokens have no tiles
+          ++wb;
+          if (wb - win_b >= 32) {
+            win_b = wb;
+            win_len = wb + lane < B ? len_of(wb + lane) : 0;
+          }
+          wL = __shfl_sync(0xffffffffu, win_len, wb - win_b);
+        } while (wL == 0 && wb < B - 1);
+        wnt = (wL + kTile - 1) / kTile;
+      }
+    }
+  };
+  if (tiles > 0) look_up();
+
+  // The cache, q and the output may be in use by the preceding kernel (programmatic dependent launch; lengths and
+  // block tables are not its outputs): wait for it before the first load of them and before any write.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  long long done_seg = wseg;  // the consumer's segment
+  for (int s = 0; s < NS; ++s)
+    if (left > 0) bring(s);
+  // sequences without a token: zeros, and a log-sum-exp of -inf
+  for (int i = cta * NW + warp; i < B; i += gridDim.x * NW) {
+    if (len_of(i) != 0) continue;
+    uint4* o4 = reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.out) + (size_t)i * p.num_q_heads * D);
+    for (int e = lane; e < p.num_q_heads * D / 8; e += 32) o4[e] = make_uint4(0, 0, 0, 0);
+    if (p.lse)
+      for (int h = lane; h < p.num_q_heads; h += 32) p.lse[(size_t)i * p.num_q_heads + h] = -INFINITY;
+  }
+
+  // ---- tiles
+  S st;
+  bool head = false;  // the current piece holds its segment's first tile
+  int k = 0;
+  for (; k < tiles; ++k) {
+    const int s = k % NS;
+    const int4 d = desc[s];
+    const int flags = d.z >> 8;
+    if (flags & F_FIRST) {  // q is on its way while the tile lands
+      st.begin(reinterpret_cast<const uint8_t*>(p.q) + ((size_t)d.x * p.num_q_heads + (size_t)d.y * G) * D * 2,
+               p.scale_log2, lane);
+      head = flags & F_HEAD;
+    }
+    if (!mbar_wait_warp(&full[s], (k / NS) & 1)) break;
+    st.template tile<LY>(ring + s * LY::STAGE, d.z & 0xff, lane);
+    __syncwarp();
+    if (left > 0) bring(s);
+    if (!(flags & F_LAST)) continue;
+    // ---- a piece is complete
+    st.finish();
+    const bool tail = flags & F_TAIL;
+    const int g = lane >> 2, c = lane & 3;
+    if (head && tail) {
+      T* out = reinterpret_cast<T*>(p.out) + ((size_t)d.x * p.num_q_heads + (size_t)d.y * G) * D;
+#pragma unroll
+      for (int nt = 0; nt < S::NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int h = 8 * nt + 2 * c + e;
+          if (h >= G) continue;
+          const float inv = 1.f / st.l[nt][e];
+#pragma unroll
+          for (int grp = 0; grp < S::NG; ++grp) {
+            float v[8];
+            st.values(nt, grp, e, v);
+            uint4 u;
+            u.x = Elt<DT>::from_f2(v[0] * inv, v[1] * inv);
+            u.y = Elt<DT>::from_f2(v[2] * inv, v[3] * inv);
+            u.z = Elt<DT>::from_f2(v[4] * inv, v[5] * inv);
+            u.w = Elt<DT>::from_f2(v[6] * inv, v[7] * inv);
+            st_v4(out + h * D + 64 * grp + 8 * g, u);
+          }
+          if (p.lse && g == 0)
+            p.lse[(size_t)d.x * p.num_q_heads + (size_t)d.y * G + h] = (st.R[nt][e] + __log2f(st.l[nt][e])) * kLn2;
+        }
+    } else {
+      const int which = k == tiles - 1;  // the warp's last piece lies in its ring, which is done with
+      float* part = reinterpret_cast<float*>(which ? smem + LY::RING_OFF + warp * LY::RING : smem + LY::PART_OFF + warp * LY::PART);
+#pragma unroll
+      for (int nt = 0; nt < S::NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int h = 8 * nt + 2 * c + e;
+          if (h >= G) continue;
+#pragma unroll
+          for (int grp = 0; grp < S::NG; ++grp) {
+            float v[8];
+            st.values(nt, grp, e, v);
+            float4* o4 = reinterpret_cast<float4*>(part + h * D + 64 * grp + 8 * g);
+            o4[0] = make_float4(v[0], v[1], v[2], v[3]);
+            o4[1] = make_float4(v[4], v[5], v[6], v[7]);
+          }
+          if (g == 0) {
+            part[G * D + h] = st.R[nt][e];
+            part[G * D + G + h] = st.l[nt][e];
+          }
+        }
+      if (lane == 0) {
+        Piece pc;
+        pc.b = d.x;
+        pc.g = d.y;
+        pc.flags = F_VALID | (head ? F_HEAD : 0) | (tail ? F_TAIL : 0);
+        pc.nt = d.w;
+        pc.seg_start = done_seg;
+        pieces[2 * warp + which] = pc;
+      }
+    }
+    done_seg += d.w;  // empty sequences take no room on the line: the next segment follows at once
+  }
+  if (k < tiles) {  // a wait ran out: record it, and wait (with the same limit) for the copies still in flight
+    if (lane == 0) PA_RECORD_ERROR(PA_ERRBIT_TIMEOUT);
+    const int brought = tiles - left;
+    for (++k; k < brought; ++k) mbar_wait_warp(&full[k % NS], (k / NS) & 1);
+  }
+  // let the next programmatically launched kernel begin its set-up; it waits for this grid before it touches memory
+  asm volatile("griddepcontrol.launch_dependents;");
+  __syncthreads();
+
+  // ---- join the pieces of each segment.  Lane i holds piece i of the CTA; a run is the pieces of one segment.
+  static_assert(NW <= 16, "a warp's lanes hold all pieces of the CTA");
+  Piece pc;
+  pc.flags = 0;
+  pc.b = pc.g = pc.nt = 0;
+  pc.seg_start = 0;
+  if (lane < 2 * NW) pc = pieces[lane];
+  const bool valid = pc.flags & F_VALID;
+  const unsigned vmask = __ballot_sync(0xffffffffu, valid);
+  const unsigned below = vmask & ((1u << lane) - 1u);
+  const long long prev = __shfl_sync(0xffffffffu, pc.seg_start, below ? 31 - __clz(below) : lane);
+  const unsigned smask = __ballot_sync(0xffffffffu, valid && (!below || prev != pc.seg_start));
+  for (int item = warp; item < __popc(smask) * G; item += NW) {
+    const int r = item / G, h = item - r * G;
+    const bool nth = (smask >> lane & 1) && __popc(smask & ((1u << lane) - 1u)) == r;
+    const int first = __ffs(__ballot_sync(0xffffffffu, nth)) - 1;
+    const unsigned after = first < 31 ? smask & ~((2u << first) - 1u) : 0u;
+    const unsigned mask = vmask & ~((1u << first) - 1u) & (after ? (1u << (__ffs(after) - 1)) - 1u : 0xffffffffu);
+    const int last = 31 - __clz(mask);
+    const float* part = reinterpret_cast<const float*>((lane & 1) ? smem + LY::RING_OFF + (lane >> 1) * LY::RING
+                                                                  : smem + LY::PART_OFF + (lane >> 1) * LY::PART);
+    const bool on = mask >> lane & 1;
+    const float R = on ? part[G * D + h] : -INFINITY, l = on ? part[G * D + G + h] : 0.f;
+    const float M = warp_max(l > 0.f ? R + __log2f(l) : -INFINITY);  // of the pieces' log-sum-exps: no overflow below
+    const float w = l > 0.f ? exp2f(R - M) : 0.f;
+    const float den = warp_sum(w * l);
+    constexpr int DPL = D / 32;
+    float acc[DPL];
+#pragma unroll
+    for (int j = 0; j < DPL; ++j) acc[j] = 0.f;
+    for (unsigned m = mask; m; m &= m - 1) {
+      const int i = __ffs(m) - 1;
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      const float* o = reinterpret_cast<const float*>((i & 1) ? smem + LY::RING_OFF + (i >> 1) * LY::RING
+                                                              : smem + LY::PART_OFF + (i >> 1) * LY::PART) +
+                       h * D + lane * DPL;
+#pragma unroll
+      for (int j = 0; j < DPL; ++j) acc[j] = fmaf(wi, o[j], acc[j]);
+    }
+    const int b = __shfl_sync(0xffffffffu, pc.b, first), gg = __shfl_sync(0xffffffffu, pc.g, first);
+    const int nt = __shfl_sync(0xffffffffu, pc.nt, first);
+    const long long seg0 = __shfl_sync(0xffffffffu, pc.seg_start, first);
+    const bool whole = (__shfl_sync(0xffffffffu, pc.flags, first) & F_HEAD) &&
+                       (__shfl_sync(0xffffffffu, pc.flags, last) & F_TAIL);
+    T* out = reinterpret_cast<T*>(p.out) + ((size_t)b * p.num_q_heads + (size_t)gg * G + h) * D + lane * DPL;
+    const size_t at = (size_t)b * p.num_q_heads + (size_t)gg * G + h;
+    auto write_out = [&](const float (&a)[DPL], float den_, float M_) {
+      const float inv = 1.f / den_;
+      uint32_t u[DPL / 2];
+#pragma unroll
+      for (int j = 0; j < DPL / 2; ++j) u[j] = Elt<DT>::from_f2(a[2 * j] * inv, a[2 * j + 1] * inv);
+      if constexpr (DPL == 4)
+        *reinterpret_cast<uint2*>(out) = make_uint2(u[0], u[1]);
+      else
+        *reinterpret_cast<uint32_t*>(out) = u[0];
+      if (p.lse && lane == 0) p.lse[at] = (M_ + __log2f(den_)) * kLn2;
+    };
+    if (whole) {
+      write_out(acc, den, M);
+      continue;
+    }
+    // this CTA's share of a segment cut between CTAs: slot segment + CTA (a CTA holds at most one share of a
+    // segment, and neighbouring segments share at most one CTA)
+    const size_t seg = (size_t)b * Hkv + gg;
+    {
+      const size_t row = (seg + cta) * G + h;
+      float* o = p.ws_o + row * D + lane * DPL;
+#pragma unroll
+      for (int j = 0; j < DPL; ++j) o[j] = acc[j];
+      if (lane == 0) {
+        p.ws_r[row] = M;
+        p.ws_l[row] = den;
+      }
+    }
+    __threadfence();  // the share is visible device-wide before it is counted
+    __syncwarp();
+    const int c0 = (int)(((seg0 + 1) * ctas - 1) / total), c1 = (int)(((seg0 + nt) * ctas - 1) / total);
+    int done = 0;
+    if (lane == 0) {
+      done = atomicAdd(p.ws_cnt + at, 1) == c1 - c0;
+      if (done) atomicExch(p.ws_cnt + at, 0);  // the next call finds the counter at zero
+    }
+    if (!__shfl_sync(0xffffffffu, done, 0)) continue;
+    __threadfence();
+    float M2 = -INFINITY;
+    for (int cc = c0 + lane; cc <= c1; cc += 32) {
+      const size_t row = (seg + cc) * G + h;
+      const float li = __ldcg(p.ws_l + row);
+      M2 = fmaxf(M2, li > 0.f ? __ldcg(p.ws_r + row) + __log2f(li) : -INFINITY);
+    }
+    M2 = warp_max(M2);
+    float den2 = 0.f;
+#pragma unroll
+    for (int j = 0; j < DPL; ++j) acc[j] = 0.f;
+    for (int cb = c0; cb <= c1; cb += 32) {
+      float w2 = 0.f;
+      if (cb + lane <= c1) {
+        const size_t row = (seg + cb + lane) * G + h;
+        const float li = __ldcg(p.ws_l + row);
+        w2 = li > 0.f ? exp2f(__ldcg(p.ws_r + row) - M2) : 0.f;
+        den2 = fmaf(w2, li, den2);
+      }
+      const int cnt = min(32, c1 - cb + 1);
+      for (int i0 = 0; i0 < cnt; i0 += 8) {  // eight shares' loads in flight
+        float v[8][DPL];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float* o = p.ws_o + ((seg + min(cb + i0 + i, c1)) * G + h) * D + lane * DPL;
+          if constexpr (DPL == 4) {
+            const float4 f = __ldcg(reinterpret_cast<const float4*>(o));
+            v[i][0] = f.x; v[i][1] = f.y; v[i][2] = f.z; v[i][3] = f.w;
+          } else {
+            const float2 f = __ldcg(reinterpret_cast<const float2*>(o));
+            v[i][0] = f.x; v[i][1] = f.y;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float wi = __shfl_sync(0xffffffffu, w2, (i0 + i) & 31);
+          if (i0 + i < cnt)
+#pragma unroll
+            for (int j = 0; j < DPL; ++j) acc[j] = fmaf(wi, v[i][j], acc[j]);
+        }
+      }
+    }
+    write_out(acc, warp_sum(den2), M2);
   }
 }
 
-bool make_plan(int batch, int Hq, int Hkv, int D, int max_context_len, int num_partitions, int* grid, size_t* bytes) {
+// ------------------------------------------------------------------ host side
+template <int D, int G>
+struct Shape {
+  static constexpr int NW = G == 16 ? 8 : 16;
+  static constexpr int NS = 2;
+};
+
+struct Plan {
+  int grid;
+  size_t off_r, off_l, off_o, bytes;
+};
+
+bool make_plan(int batch, int Hq, int Hkv, int D, int max_context_len, int num_partitions, Plan* pl) {
   if (batch < 0 || Hq <= 0 || Hkv <= 0 || num_partitions < 0 || max_context_len < 0 || Hq % Hkv) return false;
   if (!valid_head_dim(D) || !valid_group(Hq / Hkv)) return false;
-  *grid = num_partitions ? num_partitions : sm_count();
-  *bytes = 256;
+  if ((int64_t)batch * Hq >= (1ll << 31)) return false;
+  const int G = Hq / Hkv;
+  // one CTA fills an SM; no more CTAs than leave each at least four tiles (were all contexts as long as they may be)
+  const int64_t tiles = (int64_t)batch * Hkv * ((max_context_len + (int64_t)kTile - 1) / kTile);
+  pl->grid = num_partitions ? num_partitions : (int)std::max<int64_t>(1, std::min<int64_t>(sm_count(), (tiles + 3) / 4));
+  auto align256 = [](size_t x) { return (x + 255) & ~size_t(255); };
+  const size_t slots = (size_t)batch * Hkv + pl->grid;
+  pl->off_r = align256((size_t)batch * Hq * 4);
+  pl->off_l = pl->off_r + align256(slots * G * 4);
+  pl->off_o = pl->off_l + align256(slots * G * 4);
+  pl->bytes = pl->off_o + align256(slots * G * D * 4);
   return true;
+}
+
+template <int DT, int D, int G>
+int launch(const Params& p, int grid, cudaStream_t st) {
+  constexpr int NW = Shape<D, G>::NW, NS = Shape<D, G>::NS;
+  using LY = Layout<D, G, NW, NS>;
+  static_assert(LY::BYTES <= 227 * 1024, "shared memory of one CTA");
+  auto kern = decode_int4_kernel<DT, D, G, NW, NS>;
+  // per instantiation and device; host threads may race to set it, which only repeats an idempotent call
+  static std::atomic<bool> attr_set[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return PA_ERR_CUDA;
+  if (dev < 0 || dev >= 64 || !attr_set[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, LY::BYTES) != cudaSuccess)
+      return PA_ERR_CUDA;
+    if (dev >= 0 && dev < 64) attr_set[dev].store(true, std::memory_order_release);
+  }
+  return launch_programmatic(kern, dim3((unsigned)grid), dim3(NW * 32), LY::BYTES, st, p);
+}
+
+template <int DT, int D>
+int dispatch_g(int G, const Params& p, int grid, cudaStream_t st) {
+  switch (G) {
+    case 1: return launch<DT, D, 1>(p, grid, st);
+    case 2: return launch<DT, D, 2>(p, grid, st);
+    case 4: return launch<DT, D, 4>(p, grid, st);
+    case 8: return launch<DT, D, 8>(p, grid, st);
+    case 16: return launch<DT, D, 16>(p, grid, st);
+  }
+  return PA_ERR_UNSUPPORTED;
 }
 
 }  // namespace
@@ -126,23 +920,20 @@ bool make_plan(int batch, int Hq, int Hkv, int D, int max_context_len, int num_p
 extern "C" int pa_decode_int4_plan(int batch, int num_q_heads, int num_kv_heads, int head_dim, int max_context_len,
                                    int num_partitions_or_0, int* grid_out, int* max_pieces_out,
                                    size_t* workspace_bytes_out) {
-  int grid;
-  size_t bytes;
-  if (!make_plan(batch, num_q_heads, num_kv_heads, head_dim, max_context_len, num_partitions_or_0, &grid, &bytes))
+  Plan pl;
+  if (!make_plan(batch, num_q_heads, num_kv_heads, head_dim, max_context_len, num_partitions_or_0, &pl))
     return PA_ERR_INVALID;
-  if (grid_out) *grid_out = grid;
-  if (max_pieces_out) *max_pieces_out = batch * num_kv_heads + grid;
-  if (workspace_bytes_out) *workspace_bytes_out = bytes;
+  if (grid_out) *grid_out = pl.grid;
+  if (max_pieces_out) *max_pieces_out = batch * num_kv_heads + pl.grid;
+  if (workspace_bytes_out) *workspace_bytes_out = pl.bytes;
   return PA_OK;
 }
 
 extern "C" size_t pa_decode_int4_workspace_size(int batch, int num_q_heads, int num_kv_heads, int head_dim,
                                                 int max_context_len, int num_partitions_or_0) {
-  int grid;
-  size_t bytes;
-  return make_plan(batch, num_q_heads, num_kv_heads, head_dim, max_context_len, num_partitions_or_0, &grid, &bytes)
-             ? bytes
-             : 0;
+  Plan pl;
+  return make_plan(batch, num_q_heads, num_kv_heads, head_dim, max_context_len, num_partitions_or_0, &pl) ? pl.bytes
+                                                                                                         : 0;
 }
 
 extern "C" int pa_decode_int4(const void* q, const void* k_codes, const void* v_codes, const void* k_params,
@@ -169,22 +960,26 @@ extern "C" int pa_decode_int4(const void* q, const void* k_codes, const void* v_
   if (num_blocks == 0 && max_context_len > 0) return PA_ERR_INVALID;
   if ((int64_t)num_blocks * block_size >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
   if ((int64_t)max_blocks_per_seq * block_size >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
-  int grid;
-  size_t bytes;
-  if (!make_plan(batch, num_q_heads, num_kv_heads, head_dim, max_context_len, num_partitions_or_0, &grid, &bytes))
+  Plan pl;
+  if (!make_plan(batch, num_q_heads, num_kv_heads, head_dim, max_context_len, num_partitions_or_0, &pl))
     return PA_ERR_INVALID;
-  if (!workspace || workspace_bytes < bytes) return PA_ERR_WORKSPACE;
+  if (!workspace || workspace_bytes < pl.bytes) return PA_ERR_WORKSPACE;
   if (reinterpret_cast<uintptr_t>(workspace) & 255u) return PA_ERR_ALIGN;
+  uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
   Params p;
   p.q = q;
   p.out = out;
   p.lse = lse_out;
-  p.kc = (const uint8_t*)k_codes;
-  p.vc = (const uint8_t*)v_codes;
-  p.kp = (const uint32_t*)k_params;
-  p.vp = (const uint32_t*)v_params;
+  p.base[0] = (const uint8_t*)k_codes;
+  p.base[1] = (const uint8_t*)v_codes;
+  p.base[2] = (const uint8_t*)k_params;
+  p.base[3] = (const uint8_t*)v_params;
   p.block_tables = block_tables;
   p.context_lens = context_lens;
+  p.ws_cnt = reinterpret_cast<int*>(ws);
+  p.ws_r = reinterpret_cast<float*>(ws + pl.off_r);
+  p.ws_l = reinterpret_cast<float*>(ws + pl.off_l);
+  p.ws_o = reinterpret_cast<float*>(ws + pl.off_o);
   p.max_blocks_per_seq = max_blocks_per_seq;
   p.batch = batch;
   p.num_q_heads = num_q_heads;
@@ -192,8 +987,8 @@ extern "C" int pa_decode_int4(const void* q, const void* k_codes, const void* v_
   p.block_size = block_size;
   p.num_blocks = num_blocks;
   p.scale_log2 = scale * 1.4426950408889634f;
-  auto kern = dtype == PA_BF16 ? (head_dim == 128 ? decode_int4_kernel<PA_BF16, 128> : decode_int4_kernel<PA_BF16, 64>)
-                               : (head_dim == 128 ? decode_int4_kernel<PA_F16, 128> : decode_int4_kernel<PA_F16, 64>);
-  return launch_programmatic(kern, dim3((unsigned)num_kv_heads, (unsigned)batch), dim3(128), 0, (cudaStream_t)stream, p,
-                             G);
+  cudaStream_t st = (cudaStream_t)stream;
+  if (dtype == PA_BF16)
+    return head_dim == 128 ? dispatch_g<PA_BF16, 128>(G, p, pl.grid, st) : dispatch_g<PA_BF16, 64>(G, p, pl.grid, st);
+  return head_dim == 128 ? dispatch_g<PA_F16, 128>(G, p, pl.grid, st) : dispatch_g<PA_F16, 64>(G, p, pl.grid, st);
 }
