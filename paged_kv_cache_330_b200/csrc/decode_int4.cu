@@ -8,13 +8,15 @@
 //
 // Work split.  A segment is one (sequence, KV head), cut into tiles of 32 tokens; all segments end to end form
 // one line of T tiles.  CTA c takes tiles [T c / n, T (c+1) / n), its warps equal parts of that.  Every warp
-// walks its own part: it looks its blocks up, brings its tiles in with bulk copies into a ring of its own
-// (one mbarrier per stage, no other warp involved) and keeps the softmax state and the output of the current
-// segment in registers.  What a warp holds of a segment is a piece: a whole segment is written out at once, a
-// partial one goes to shared memory, and after the one barrier at the end of the CTA the pieces of a segment
-// are joined, first within the CTA, then, for the at most two segments that a CTA shares with its neighbours,
-// through the workspace by the CTA that finishes last (a counter per head, no waiting).  The joining order is
-// the order of the line, so results do not depend on timing.
+// walks its own part: it looks its blocks up, brings its tiles into a ring of its own with asynchronous 16-byte
+// copies (cp.async, nine a lane per tile; no other warp involved) and keeps the softmax state and the output of
+// the current segment in registers.  Bulk copies were measured first: one instruction per copy, but each of a
+// tile's eight takes a turn of its own through the uniform path, 200 of the 700 instructions of a tile.
+// What a warp holds of a segment is a piece: a whole segment is written out at once, a partial one goes to
+// shared memory, and after the one barrier at the end of the tiles the pieces of a segment are joined, first
+// within the CTA, then, for the at most two segments that a CTA shares with its neighbours, through the
+// workspace by the CTA that finishes last (a counter per segment, no waiting).  The joining order is the order
+// of the line, so results do not depend on timing.
 //
 // Mathematics.  Products run on mma.m16n8k16 (fp16 in, fp32 out) with tokens (scores) or columns (PV) as the 16
 // rows and up to 8 heads of the group as the 8 columns; G 16 takes two column tiles.
@@ -26,10 +28,10 @@
 //   * PV: the weight of a token enters times its V scale, P' = 2^(x - R) s_V in fp16 (rounded once, 2^-11; its
 //     rounded value also multiplies the zero point, so code and zero-point parts carry the same rounding and
 //     the error stays relative to the value, not to the code):  O += P' code,  Z += P' z_V (fp32).
-//   * Online softmax with a reference R per head that moves only when it must: R is set from a piece's first
-//     tile so that its largest P' lies in (2^3, 2^4], and is raised only when some P' reaches 2^15 or the sum l
-//     passes 2^100.  Any R gives the same quotient O / l; the usual tile needs no maximum, no shuffles and no
-//     rescaling of O, one vote tells.  l and O are fp32.
+//   * Online softmax with a reference R per head that moves only when it must: a piece starts with a guess, which
+//     stays if it puts the first tile's largest P' into [2^3, 2^15) and is set so (to (2^3, 2^4]) otherwise; later R
+//     is raised only when P' come near 2^15 or the sum l passes 2^100.  Any R gives the same quotient O / l;
+//     the usual tile needs no maximum, no shuffles and no rescaling of O, one vote tells.  l and O are fp32.
 
 #include <algorithm>
 #include <atomic>
@@ -44,7 +46,9 @@ namespace {
 using namespace pa;
 
 constexpr int kTile = 32;            // tokens per tile: two 16-token chunks, each within one block
+constexpr int kLens = 1024;           // sequences whose lengths a CTA keeps in shared memory
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kGuess = -8.f;       // a piece's first reference: fits when its largest weight * V scale is 2^-5 .. 2^7
 constexpr float kUnit = 16777216.f;  // 2^24: what a code's fp16 subnormal stands for, inverted
 
 struct Params {
@@ -54,7 +58,7 @@ struct Params {
   const uint8_t* base[4];  // K codes, V codes, K parameters, V parameters
   const int32_t* block_tables;
   const int32_t* context_lens;
-  int* ws_cnt;   // [batch * Hq] CTAs that have added their share of a head (zero between calls)
+  int* ws_cnt;   // [batch * Hkv] CTAs that have added their share of a segment (zero between calls)
   float* ws_r;   // [slots][G] reference R of a share
   float* ws_l;   // [slots][G]
   float* ws_o;   // [slots][G][D]
@@ -82,28 +86,20 @@ struct Layout {
   static constexpr int PART_OFF = RING_OFF + NW * RING;          // the first piece of every warp
   static constexpr int PIECE_OFF = (PART_OFF + NW * PART + 15) / 16 * 16;  // Piece [NW][2]
   static constexpr int DESC_OFF = PIECE_OFF + NW * 2 * (int)sizeof(Piece);  // int4 [NW][NS]
-  static constexpr int BAR_OFF = DESC_OFF + NW * NS * 16;        // full [NW][NS]
-  static constexpr int START_OFF = BAR_OFF + NW * NS * 8;        // Start [NW]: where each warp begins
+  static constexpr int START_OFF = DESC_OFF + NW * NS * 16;      // Start [NW]: where each warp begins
   static constexpr int SCAN_OFF = START_OFF + NW * 16;           // int64 [NW]
-  static constexpr int BYTES = SCAN_OFF + NW * 8;
+  static constexpr int DONE_OFF = SCAN_OFF + NW * 8;             // int [2]: segments this CTA joins from the workspace
+  static constexpr int LENS_OFF = DONE_OFF + 8;                  // int [kLens]: lengths, for batches that fit
+  static constexpr int BYTES = LENS_OFF + kLens * 4;
+  // Byte offset of word `word` (4 bytes) of row `row` among a tile's codes: 16-byte units of a row are exchanged so
+  // that neighbouring rows' units lie in different banks.  Rows 8 apart are exchanged alike.
+  static __device__ __forceinline__ int code_off(int row, int word) {
+    const int unit = word >> 2;
+    return row * ROWB + ((ROWB == 64 ? unit ^ (row >> 1 & 3) : unit ^ (row >> 2 & 1)) << 4) + (word & 3) * 4;
+  }
   static_assert(STAGE % 128 == 0 && sizeof(Piece) % 8 == 0 && PIECE_OFF % 8 == 0, "alignment");
 };
 
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   uint32_t d;
   asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
@@ -115,6 +111,14 @@ __device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The same; `first` (a constant where it is called): from a zero accumulator.
+__device__ __forceinline__ void mma_f16(bool first, float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+  if (!first) return mma_f16(c, a0, a1, a2, a3, b0, b1);
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t trans8x8(uint32_t a) {
   uint32_t d;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
@@ -124,10 +128,8 @@ __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ uint32_t hmax2_bits(uint32_t a, uint32_t b) {
-  const __half2 h = __hmax2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
+__device__ __forceinline__ __half2 as_h2(uint32_t a) { return *reinterpret_cast<const __half2*>(&a); }
+__device__ __forceinline__ uint32_t as_u32(__half2 a) { return *reinterpret_cast<const uint32_t*>(&a); }
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
@@ -148,10 +150,18 @@ __device__ __forceinline__ float rows_sum(float v) {
   for (int o = 4; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Floor division of a >= 0 by b > 0; `narrow` (uniform) says both fit in 32 bits: the 64-bit one is a long sequence.
+__device__ __forceinline__ long long udiv(long long a, long long b, bool narrow) {
+  return narrow ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
 constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;  // a nibble of each half, worth 2^-24 and 2^-20
@@ -173,7 +183,8 @@ struct State {
   __device__ __forceinline__ void begin(const uint8_t* qrows, float scale_log2, int lane) {
     const int g = lane >> 2, c = lane & 3;
     uint4 raw[NT][WPL];
-    float amax = 0.f;
+    using T2 = typename Elt<DT>::T2;
+    uint32_t top = 0;  // largest magnitudes, two columns at once
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -190,11 +201,12 @@ struct State {
         const uint32_t w[4] = {raw[nt][i].x, raw[nt][i].y, raw[nt][i].z, raw[nt][i].w};
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-          const float2 f = Elt<DT>::to_f2(w[m]);
-          amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+          const T2 v = __hmax2(*reinterpret_cast<T2*>(&top), __habs2(*reinterpret_cast<const T2*>(&w[m])));
+          top = *reinterpret_cast<const uint32_t*>(&v);
         }
       }
-    amax = warp_max(amax);
+    const float2 top2 = Elt<DT>::to_f2(top);
+    const float amax = warp_max(fmaxf(top2.x, top2.y));
     int e = 0;
     if (amax > 0.f) {
       int k;
@@ -223,19 +235,21 @@ struct State {
       }
 #pragma unroll
       for (int grp = 0; grp < NG; ++grp) {
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        float acc[4];
 #pragma unroll
         for (int i = grp; i < WPL; i += NG)
 #pragma unroll
           for (int s = 0; s < 2; ++s)
-            mma_f16(acc, 0x00010001u, 0x00010001u, 0x00100010u, 0x00100010u, qb[nt][2 * i + s][0], qb[nt][2 * i + s][1]);
+            mma_f16(i == grp && s == 0, acc, 0x00010001u, 0x00010001u, 0x00100010u, 0x00100010u, qb[nt][2 * i + s][0],
+                    qb[nt][2 * i + s][1]);
         qsum[nt][grp][0] = acc[0];
         qsum[nt][grp][1] = acc[1];
         z[nt][grp][0] = z[nt][grp][1] = 0.f;
       }
 #pragma unroll
       for (int i = 0; i < KS; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
-      l[nt][0] = l[nt][1] = R[nt][0] = R[nt][1] = 0.f;
+      l[nt][0] = l[nt][1] = 0.f;
+      R[nt][0] = R[nt][1] = kGuess;
     }
     fresh = true;
   }
@@ -285,30 +299,30 @@ struct State {
     fresh = __any_sync(0xffffffffu, still);
   }
 
-  // One tile at shared address `st` (a stage), nv of its 32 tokens valid.
+  // One tile in shared memory at `st` (a stage), nv of its 32 tokens valid.
   template <typename LY>
-  __device__ __forceinline__ void tile(uint32_t st, int nv, int lane) {
+  __device__ __forceinline__ void tile(const uint8_t* st, int nv, int lane) {
     const int g = lane >> 2, c = lane & 3;
     // ---- scores: rows tokens g, g + 8, g + 16, g + 24 (r = 2 mt + hh), columns heads 8nt + 2c + {0,1}
+    const uint8_t* kl = st + LY::K_OFF + LY::code_off(g, WPL * c);
+    const uint8_t* kpl = st + LY::KP_OFF + g * LY::PARB;
+    const uint8_t* vpl = st + LY::VP_OFF + g * LY::PARB;
     float x[2][NT][4];
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt) {
-      const uint32_t ra = st + LY::K_OFF + (16 * mt + g) * LY::ROWB + 4 * WPL * c, rb = ra + 8 * LY::ROWB;
+      const uint8_t* ra = kl + 16 * mt * LY::ROWB;
+      const uint8_t* rb = ra + 8 * LY::ROWB;
       uint32_t wa[WPL], wb[WPL];
       if constexpr (WPL == 4) {
-        const uint4 a = lds128(ra), b = lds128(rb);
+        const uint4 a = *reinterpret_cast<const uint4*>(ra), b = *reinterpret_cast<const uint4*>(rb);
         wa[0] = a.x; wa[1] = a.y; wa[2] = a.z; wa[3] = a.w;
         wb[0] = b.x; wb[1] = b.y; wb[2] = b.z; wb[3] = b.w;
       } else {
-        const uint2 a = lds64(ra), b = lds64(rb);
+        const uint2 a = *reinterpret_cast<const uint2*>(ra), b = *reinterpret_cast<const uint2*>(rb);
         wa[0] = a.x; wa[1] = a.y;
         wb[0] = b.x; wb[1] = b.y;
       }
       float acc[NT][NG][4];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int grp = 0; grp < NG; ++grp) acc[nt][grp][0] = acc[nt][grp][1] = acc[nt][grp][2] = acc[nt][grp][3] = 0.f;
 #pragma unroll
       for (int i = 0; i < WPL; ++i)
 #pragma unroll
@@ -316,19 +330,19 @@ struct State {
           const uint32_t a = wa[i] >> (8 * s), b = wb[i] >> (8 * s);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
-            mma_f16(acc[nt][i % NG], a & kLow, b & kLow, a & kHigh, b & kHigh, qb[nt][2 * i + s][0],
+            mma_f16(i < NG && s == 0, acc[nt][i % NG], a & kLow, b & kLow, a & kHigh, b & kHigh, qb[nt][2 * i + s][0],
                     qb[nt][2 * i + s][1]);
         }
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
-        const uint32_t pa = st + LY::KP_OFF + (16 * mt + 8 * hh + g) * LY::PARB;
+        const uint8_t* pa = kpl + (16 * mt + 8 * hh) * LY::PARB;
         float2 par[NG];
         if constexpr (NG == 2) {
-          const uint2 w = lds64(pa);
+          const uint2 w = *reinterpret_cast<const uint2*>(pa);
           par[0] = Elt<DT>::to_f2(w.x);
           par[1] = Elt<DT>::to_f2(w.y);
         } else {
-          par[0] = Elt<DT>::to_f2(lds32(pa));
+          par[0] = Elt<DT>::to_f2(*reinterpret_cast<const uint32_t*>(pa));
         }
 #pragma unroll
         for (int grp = 0; grp < NG; ++grp) {
@@ -346,14 +360,14 @@ struct State {
     float sv[4][NG], zv[4][NG];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const uint32_t pa = st + LY::VP_OFF + (8 * r + g) * LY::PARB;
+      const uint8_t* pa = vpl + 8 * r * LY::PARB;
       uint32_t w[NG];
       if constexpr (NG == 2) {
-        const uint2 u = lds64(pa);
+        const uint2 u = *reinterpret_cast<const uint2*>(pa);
         w[0] = u.x;
         w[1] = u.y;
       } else {
-        w[0] = lds32(pa);
+        w[0] = *reinterpret_cast<const uint32_t*>(pa);
       }
 #pragma unroll
       for (int grp = 0; grp < NG; ++grp) {
@@ -376,7 +390,7 @@ struct State {
     uint32_t pk[NT][NG][4];
     float sum[NT][2];
     auto weights = [&]() -> bool {
-      uint32_t big = 0;
+      __half2 all = as_h2(0u);  // the sum of all P', at least each of them
       bool over = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -390,14 +404,31 @@ struct State {
 #pragma unroll
           for (int grp = 0; grp < NG; ++grp) {
             pk[nt][grp][r] = pack_h2(p0 * sv[r][grp], p1 * sv[r][grp]);
-            big = hmax2_bits(big, pk[nt][grp][r]);
+            all = __hadd2(all, as_h2(pk[nt][grp][r]));
           }
         }
         over |= !(sum[nt][0] < 1.2676506e30f) || !(sum[nt][1] < 1.2676506e30f);  // 2^100
       }
-      return over || ((big + 0x08000800u) & 0x80008000u) != 0;  // some P' of 2^15 or more
+      return over || ((as_u32(all) + 0x08000800u) & 0x80008000u) != 0;  // 2^15 or more (exponent bits 1111x)
     };
-    if (__any_sync(0xffffffffu, weights() || fresh)) {
+    bool move = __any_sync(0xffffffffu, weights());
+    if (fresh && !move) {  // is the guess large enough for every head?
+      bool low = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        __half2 top = as_h2(0u);
+#pragma unroll
+        for (int grp = 0; grp < NG; ++grp)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) top = __hmax2(top, as_h2(pk[nt][grp][r]));
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) top = __hmax2(top, as_h2(__shfl_xor_sync(0xffffffffu, as_u32(top), o)));
+        low |= !(__low2float(top) >= 8.f) || !(__high2float(top) >= 8.f);
+      }
+      move = __any_sync(0xffffffffu, low);
+      fresh = move;
+    }
+    if (move) {
       float svm[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) svm[r] = NG == 2 ? fmaxf(sv[r][0], sv[r][NG - 1]) : sv[r][0];
@@ -412,7 +443,7 @@ struct State {
       for (int grp = 0; grp < NG; ++grp)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&pk[nt][grp][r]));
+          const float2 p = __half22float2(as_h2(pk[nt][grp][r]));
           z[nt][grp][0] = fmaf(p.x, zv[r][grp], z[nt][grp][0]);
           z[nt][grp][1] = fmaf(p.y, zv[r][grp], z[nt][grp][1]);
           pk[nt][grp][r] = trans8x8(pk[nt][grp][r]);  // tokens along the rows of the B operand
@@ -420,25 +451,32 @@ struct State {
     }
     // ---- O^T += V^T P'^T: tokens 2c, 2c + 1, 2c + 8, 2c + 9 of each half; word `grp` of lane g's piece of a row holds
     // values 64 grp + 8 g ..
+    // (codes lie swizzled, see bring; odd c take their two tokens in the other order, which with the swizzle spreads
+    // a half-warp's 8-byte loads over all banks and costs only another permute selector)
+    const int odd = c & 1;
+    const uint8_t* vl = st + LY::V_OFF;
+    const uint8_t* v0 = vl + LY::code_off(2 * c + odd, NG * g);
+    const uint8_t* v1 = vl + LY::code_off(2 * c + (odd ^ 1), NG * g);
+    const uint32_t sel_lo = odd ? 0x1054u : 0x5410u, sel_hi = odd ? 0x3276u : 0x7632u;
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt) {
       uint32_t w[4][NG];
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const uint32_t a = st + LY::V_OFF + (16 * mt + 2 * c + (t & 1) + 8 * (t >> 1)) * LY::ROWB + 4 * NG * g;
+        const uint8_t* a = ((t & 1) ? v1 : v0) + (16 * mt + 8 * (t >> 1)) * LY::ROWB;
         if constexpr (NG == 2) {
-          const uint2 u = lds64(a);
+          const uint2 u = *reinterpret_cast<const uint2*>(a);
           w[t][0] = u.x;
           w[t][1] = u.y;
         } else {
-          w[t][0] = lds32(a);
+          w[t][0] = *reinterpret_cast<const uint32_t*>(a);
         }
       }
 #pragma unroll
       for (int grp = 0; grp < NG; ++grp)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          const uint32_t sel = half ? 0x7632u : 0x5410u;
+          const uint32_t sel = half ? sel_hi : sel_lo;
           const uint32_t a = prmt(w[0][grp], w[1][grp], sel), b = prmt(w[2][grp], w[3][grp], sel);
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
@@ -481,7 +519,6 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
   using T = typename Elt<DT>::T;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + LY::BAR_OFF) + warp * NS;
   struct Start {
     long long pre;  // tiles of all sequences before b, per KV head
     int b;
@@ -492,22 +529,22 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
   const int B = p.batch, Hkv = p.num_kv_heads, bs = p.block_size;
   const int cap = p.max_blocks_per_seq * bs;
 
-  if (lane == 0) {
-    for (int i = 0; i < NS; ++i) mbar_init(&full[i], 1);
-    fence_mbar_init();
-    pieces[2 * warp].flags = pieces[2 * warp + 1].flags = 0;
-  }
+  int* lens_s = reinterpret_cast<int*>(smem + LY::LENS_OFF);
+  int* done_s = reinterpret_cast<int*>(smem + LY::DONE_OFF);
+  if (lane == 0) pieces[2 * warp].flags = pieces[2 * warp + 1].flags = 0;
 
   // ---- the line: thread i counts the tiles of sequences [i * per, (i + 1) * per); a scan over the threads
   const int per = (B + NW * 32 - 1) / (NW * 32);
   const int i0 = min(B, (int)threadIdx.x * per), i1 = min(B, i0 + per);
-  auto len_of = [&](int i) { return min(max(__ldg(p.context_lens + i), 0), cap); };
+  auto len_of = [&](int i) { return i < kLens ? lens_s[i] : min(max(__ldg(p.context_lens + i), 0), cap); };
   long long mine = 0;
   bool clamped = false;
   for (int i = i0; i < i1; ++i) {
     const int L = __ldg(p.context_lens + i);
-    clamped |= L < 0 || L > cap;
-    mine += (min(max(L, 0), cap) + kTile - 1) / kTile;
+    const int Lc = min(max(L, 0), cap);
+    clamped |= L != Lc;
+    if (i < kLens) lens_s[i] = Lc;
+    mine += (Lc + kTile - 1) / kTile;
   }
   if (clamped && cta == 0) PA_RECORD_ERROR(PA_ERRBIT_INDEX);
   long long incl = mine;
@@ -526,10 +563,11 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
   }
   total *= Hkv;
   const long long ctas = min((long long)gridDim.x, total);  // at least one tile for each CTA that takes part
+  const bool narrow = (total + 1) * (ctas + 1) < (1ll << 32);
   long long x0 = 0, n = 0;
   if (cta < ctas) {
-    x0 = total * cta / ctas;
-    n = total * (cta + 1) / ctas - x0;
+    x0 = udiv(total * cta, ctas, narrow);
+    n = udiv(total * (cta + 1), ctas, narrow) - x0;
   }
   const long long lo = (before + incl - mine) * Hkv, hi = (before + incl) * Hkv;
   for (int w = 0; w < NW; ++w) {
@@ -561,17 +599,28 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
     wL = __shfl_sync(0xffffffffu, win_len, 0);
     wnt = (wL + kTile - 1) / kTile;
     const long long in_seq = xs - starts[warp].pre * Hkv;
-    wg = (int)(in_seq / wnt);
+    wg = (int)udiv(in_seq, wnt, narrow);
     wt = (int)(in_seq - (long long)wg * wnt);
     wseg = xs - wt;
   }
   const uint32_t ring = smem_u32(smem + LY::RING_OFF) + warp * LY::RING;
   int4* desc = reinterpret_cast<int4*>(smem + LY::DESC_OFF) + warp * NS;
   const int bs_shift = __ffs(bs) - 1;
-  const int kind = lane & 3;  // what this lane copies of chunk lane / 4 of a tile (lanes 0 .. 7)
-  const uint32_t rowb = kind < 2 ? LY::ROWB : LY::PARB;
-  const uint8_t* kind_base = p.base[kind];
-  const uint32_t kind_off = kind == 0 ? LY::K_OFF : (kind == 1 ? LY::V_OFF : (kind == 2 ? LY::KP_OFF : LY::VP_OFF));
+  const uint32_t code_block = Hkv * bs * LY::ROWB, par_block = Hkv * bs * LY::PARB;  // bytes; below 2^31 (host check)
+  // what this lane copies of a 16-token chunk: codes in 16-byte units lane, lane + 32, .. of the chunk's 16 * ROWB
+  // bytes (K and V alike); parameters: one unit of the tile's four runs
+  constexpr int UNITS = LY::ROWB, PER = UNITS / 32 > 0 ? UNITS / 32 : 1;  // code units per chunk, and per lane
+  constexpr int UPR = LY::ROWB / 16, PUNITS = LY::PARB;                   // units per row; parameter units per chunk
+  static_assert(UNITS % 32 == 0, "whole warps copy a chunk's codes");
+  const int par_run = lane / PUNITS, par_unit = lane % PUNITS;            // run: K chunk 0, K chunk 1, V chunk 0, V chunk 1
+  const uint8_t* par_base = p.base[(par_run & 2) ? 3 : 2] + par_unit * 16;
+  const uint32_t par_dst = ((par_run & 2) ? LY::VP_OFF : LY::KP_OFF) + (par_run & 1) * 16 * LY::PARB + par_unit * 16;
+  uint32_t code_dst[PER];
+#pragma unroll
+  for (int e = 0; e < PER; ++e) {
+    const int u = lane + 32 * e;
+    code_dst[e] = LY::code_off(u / UPR, (u % UPR) * 4);
+  }
 
   auto look_up = [&]() {  // block-table entries of the next 32 chunks of the walk's sequence
     win_base = 2 * wt;
@@ -584,21 +633,31 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
     const int nv = min(kTile, wL - wt * kTile), chunks = nv > 16 ? 2 : 1;
     const int flags = (piece_start ? F_FIRST : 0) | (wt == wnt - 1 || left == 1 ? F_LAST : 0) |
                       (wt == 0 ? F_HEAD : 0) | (wt == wnt - 1 ? F_TAIL : 0);
-    if (lane == 0) {
-      desc[s] = make_int4(wb, wg, nv | flags << 8, wnt);
-      mbar_arrive_expect_tx(&full[s], chunks * 16 * 2 * (LY::ROWB + LY::PARB));
-    }
-    int phys = __shfl_sync(0xffffffffu, win_phys, (2 * wt - win_base + (lane >> 2)) & 31);
-    __syncwarp();
+    if (lane == 0) desc[s] = make_int4(wb, wg, nv | flags << 8, wnt);
     const uint32_t stage = ring + s * LY::STAGE;
-    if (lane < 4 * chunks) {
-      if (phys < 0 || phys >= p.num_blocks) {  // broken caller invariant: record, read block 0 instead
-        PA_RECORD_ERROR(PA_ERRBIT_INDEX);
-        phys = 0;
+    const int at = 2 * wt - win_base;
+    int phys = __shfl_sync(0xffffffffu, win_phys, (at + (lane & 1)) & 31);
+    if (phys < 0 || phys >= p.num_blocks) {  // broken caller invariant: record, read block 0 instead
+      if ((lane & 1) < chunks) PA_RECORD_ERROR(PA_ERRBIT_INDEX);
+      phys = 0;
+    }
+#pragma unroll
+    for (int ch = 0; ch < 2; ++ch) {
+      if (ch >= chunks) break;
+      const uint32_t ph = __shfl_sync(0xffffffffu, phys, ch);
+      const uint32_t row = wg * bs + ((wt * kTile + 16 * ch) & (bs - 1));
+      const uint64_t off = (uint64_t)ph * code_block + (row * LY::ROWB + lane * 16);
+#pragma unroll
+      for (int e = 0; e < PER; ++e) {
+        cp_async16(stage + LY::K_OFF + ch * 16 * LY::ROWB + code_dst[e], p.base[0] + off + 512 * e);
+        cp_async16(stage + LY::V_OFF + ch * 16 * LY::ROWB + code_dst[e], p.base[1] + off + 512 * e);
       }
-      const int tok = wt * kTile + (lane >> 2) * 16;
-      const size_t row = ((size_t)phys * Hkv + wg) * bs + (tok & (bs - 1));
-      bulk_load(stage + kind_off + (lane >> 2) * 16 * rowb, kind_base + row * rowb, 16 * rowb, &full[s]);
+    }
+    {
+      const uint32_t ph = __shfl_sync(0xffffffffu, phys, par_run & 1);
+      const uint32_t row = wg * bs + ((wt * kTile + 16 * (par_run & 1)) & (bs - 1));
+      if (par_run < 4 && (par_run & 1) < chunks)
+        cp_async16(stage + par_dst, par_base + (uint64_t)ph * par_block + row * LY::PARB);
     }
     // step on
     --left;
@@ -628,8 +687,10 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
   // block tables are not its outputs): wait for it before the first load of them and before any write.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   long long done_seg = wseg;  // the consumer's segment
-  for (int s = 0; s < NS; ++s)
+  for (int s = 0; s < NS; ++s) {
     if (left > 0) bring(s);
+    cp_async_commit();
+  }
   // sequences without a token: zeros, and a log-sum-exp of -inf
   for (int i = cta * NW + warp; i < B; i += gridDim.x * NW) {
     if (len_of(i) != 0) continue;
@@ -642,20 +703,21 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
   // ---- tiles
   S st;
   bool head = false;  // the current piece holds its segment's first tile
-  int k = 0;
-  for (; k < tiles; ++k) {
+  for (int k = 0; k < tiles; ++k) {
     const int s = k % NS;
-    const int4 d = desc[s];
+    const int4 d = desc[s];  // written by this warp, before an earlier warp barrier
     const int flags = d.z >> 8;
     if (flags & F_FIRST) {  // q is on its way while the tile lands
       st.begin(reinterpret_cast<const uint8_t*>(p.q) + ((size_t)d.x * p.num_q_heads + (size_t)d.y * G) * D * 2,
                p.scale_log2, lane);
       head = flags & F_HEAD;
     }
-    if (!mbar_wait_warp(&full[s], (k / NS) & 1)) break;
-    st.template tile<LY>(ring + s * LY::STAGE, d.z & 0xff, lane);
+    cp_async_wait<NS - 1>();
+    __syncwarp();
+    st.template tile<LY>(smem + LY::RING_OFF + warp * LY::RING + s * LY::STAGE, d.z & 0xff, lane);
     __syncwarp();
     if (left > 0) bring(s);
+    cp_async_commit();
     if (!(flags & F_LAST)) continue;
     // ---- a piece is complete
     st.finish();
@@ -718,11 +780,6 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
     }
     done_seg += d.w;  // empty sequences take no room on the line: the next segment follows at once
   }
-  if (k < tiles) {  // a wait ran out: record it, and wait (with the same limit) for the copies still in flight
-    if (lane == 0) PA_RECORD_ERROR(PA_ERRBIT_TIMEOUT);
-    const int brought = tiles - left;
-    for (++k; k < brought; ++k) mbar_wait_warp(&full[k % NS], (k / NS) & 1);
-  }
   // let the next programmatically launched kernel begin its set-up; it waits for this grid before it touches memory
   asm volatile("griddepcontrol.launch_dependents;");
   __syncthreads();
@@ -739,120 +796,161 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
   const unsigned below = vmask & ((1u << lane) - 1u);
   const long long prev = __shfl_sync(0xffffffffu, pc.seg_start, below ? 31 - __clz(below) : lane);
   const unsigned smask = __ballot_sync(0xffffffffu, valid && (!below || prev != pc.seg_start));
-  for (int item = warp; item < __popc(smask) * G; item += NW) {
-    const int r = item / G, h = item - r * G;
+  const int runs = __popc(smask);
+  auto run_first = [&](int r) {
     const bool nth = (smask >> lane & 1) && __popc(smask & ((1u << lane) - 1u)) == r;
-    const int first = __ffs(__ballot_sync(0xffffffffu, nth)) - 1;
+    return __ffs(__ballot_sync(0xffffffffu, nth)) - 1;
+  };
+  auto run_mask = [&](int first) {
     const unsigned after = first < 31 ? smask & ~((2u << first) - 1u) : 0u;
-    const unsigned mask = vmask & ~((1u << first) - 1u) & (after ? (1u << (__ffs(after) - 1)) - 1u : 0xffffffffu);
-    const int last = 31 - __clz(mask);
-    const float* part = reinterpret_cast<const float*>((lane & 1) ? smem + LY::RING_OFF + (lane >> 1) * LY::RING
-                                                                  : smem + LY::PART_OFF + (lane >> 1) * LY::PART);
+    return vmask & ~((1u << first) - 1u) & (after ? (1u << (__ffs(after) - 1)) - 1u : 0xffffffffu);
+  };
+  auto is_whole = [&](int first, unsigned mask) {
+    return (__shfl_sync(0xffffffffu, pc.flags, first) & F_HEAD) &&
+           (__shfl_sync(0xffffffffu, pc.flags, 31 - __clz(mask)) & F_TAIL);
+  };
+  auto part_of = [&](int i) {
+    return reinterpret_cast<const float*>((i & 1) ? smem + LY::RING_OFF + (i >> 1) * LY::RING
+                                                  : smem + LY::PART_OFF + (i >> 1) * LY::PART);
+  };
+  constexpr int DPL = D / 32;
+  for (int item = warp; item < runs * G; item += NW) {
+    const int r = item / G, h = item - r * G;
+    const int first = run_first(r);
+    const unsigned mask = run_mask(first);
     const bool on = mask >> lane & 1;
+    const float* part = part_of(on ? lane : first);
     const float R = on ? part[G * D + h] : -INFINITY, l = on ? part[G * D + G + h] : 0.f;
     const float M = warp_max(l > 0.f ? R + __log2f(l) : -INFINITY);  // of the pieces' log-sum-exps: no overflow below
     const float w = l > 0.f ? exp2f(R - M) : 0.f;
     const float den = warp_sum(w * l);
-    constexpr int DPL = D / 32;
     float acc[DPL];
 #pragma unroll
     for (int j = 0; j < DPL; ++j) acc[j] = 0.f;
     for (unsigned m = mask; m; m &= m - 1) {
       const int i = __ffs(m) - 1;
       const float wi = __shfl_sync(0xffffffffu, w, i);
-      const float* o = reinterpret_cast<const float*>((i & 1) ? smem + LY::RING_OFF + (i >> 1) * LY::RING
-                                                              : smem + LY::PART_OFF + (i >> 1) * LY::PART) +
-                       h * D + lane * DPL;
+      const float* o = part_of(i) + h * D + lane * DPL;
 #pragma unroll
       for (int j = 0; j < DPL; ++j) acc[j] = fmaf(wi, o[j], acc[j]);
     }
     const int b = __shfl_sync(0xffffffffu, pc.b, first), gg = __shfl_sync(0xffffffffu, pc.g, first);
-    const int nt = __shfl_sync(0xffffffffu, pc.nt, first);
-    const long long seg0 = __shfl_sync(0xffffffffu, pc.seg_start, first);
-    const bool whole = (__shfl_sync(0xffffffffu, pc.flags, first) & F_HEAD) &&
-                       (__shfl_sync(0xffffffffu, pc.flags, last) & F_TAIL);
-    T* out = reinterpret_cast<T*>(p.out) + ((size_t)b * p.num_q_heads + (size_t)gg * G + h) * D + lane * DPL;
-    const size_t at = (size_t)b * p.num_q_heads + (size_t)gg * G + h;
-    auto write_out = [&](const float (&a)[DPL], float den_, float M_) {
-      const float inv = 1.f / den_;
-      uint32_t u[DPL / 2];
+    if (is_whole(first, mask)) {
+      const size_t at = (size_t)b * p.num_q_heads + (size_t)gg * G + h;
+      T* out = reinterpret_cast<T*>(p.out) + at * D + lane * DPL;
+      const float inv = 1.f / den;
 #pragma unroll
-      for (int j = 0; j < DPL / 2; ++j) u[j] = Elt<DT>::from_f2(a[2 * j] * inv, a[2 * j + 1] * inv);
-      if constexpr (DPL == 4)
-        *reinterpret_cast<uint2*>(out) = make_uint2(u[0], u[1]);
-      else
-        *reinterpret_cast<uint32_t*>(out) = u[0];
-      if (p.lse && lane == 0) p.lse[at] = (M_ + __log2f(den_)) * kLn2;
-    };
-    if (whole) {
-      write_out(acc, den, M);
-      continue;
-    }
-    // this CTA's share of a segment cut between CTAs: slot segment + CTA (a CTA holds at most one share of a
-    // segment, and neighbouring segments share at most one CTA)
-    const size_t seg = (size_t)b * Hkv + gg;
-    {
-      const size_t row = (seg + cta) * G + h;
-      float* o = p.ws_o + row * D + lane * DPL;
+      for (int j = 0; j < DPL / 2; ++j)
+        reinterpret_cast<uint32_t*>(out)[j] = Elt<DT>::from_f2(acc[2 * j] * inv, acc[2 * j + 1] * inv);
+      if (p.lse && lane == 0) p.lse[at] = (M + __log2f(den)) * kLn2;
+    } else {
+      // this CTA's share of a segment cut between CTAs: slot segment + CTA (a CTA holds at most one share of a
+      // segment, and neighbouring segments share at most one CTA)
+      const size_t row = ((size_t)b * Hkv + gg + cta) * G + h;
 #pragma unroll
-      for (int j = 0; j < DPL; ++j) o[j] = acc[j];
+      for (int j = 0; j < DPL; ++j) p.ws_o[row * D + lane * DPL + j] = acc[j];
       if (lane == 0) {
         p.ws_r[row] = M;
         p.ws_l[row] = den;
       }
     }
-    __threadfence();  // the share is visible device-wide before it is counted
-    __syncwarp();
-    const int c0 = (int)(((seg0 + 1) * ctas - 1) / total), c1 = (int)(((seg0 + nt) * ctas - 1) / total);
-    int done = 0;
-    if (lane == 0) {
-      done = atomicAdd(p.ws_cnt + at, 1) == c1 - c0;
-      if (done) atomicExch(p.ws_cnt + at, 0);  // the next call finds the counter at zero
-    }
-    if (!__shfl_sync(0xffffffffu, done, 0)) continue;
-    __threadfence();
-    float M2 = -INFINITY;
-    for (int cc = c0 + lane; cc <= c1; cc += 32) {
-      const size_t row = (seg + cc) * G + h;
-      const float li = __ldcg(p.ws_l + row);
-      M2 = fmaxf(M2, li > 0.f ? __ldcg(p.ws_r + row) + __log2f(li) : -INFINITY);
-    }
-    M2 = warp_max(M2);
-    float den2 = 0.f;
-#pragma unroll
-    for (int j = 0; j < DPL; ++j) acc[j] = 0.f;
-    for (int cb = c0; cb <= c1; cb += 32) {
-      float w2 = 0.f;
-      if (cb + lane <= c1) {
-        const size_t row = (seg + cb + lane) * G + h;
-        const float li = __ldcg(p.ws_l + row);
-        w2 = li > 0.f ? exp2f(__ldcg(p.ws_r + row) - M2) : 0.f;
-        den2 = fmaf(w2, li, den2);
+  }
+  if (runs == 0) return;
+  // ---- the segments cut between CTAs: the first and the last run at most
+  const int first0 = run_first(0), first1 = run_first(runs - 1);
+  const bool cut0 = !is_whole(first0, run_mask(first0)), cut1 = runs > 1 && !is_whole(first1, run_mask(first1));
+  if (!cut0 && !cut1) return;
+  __syncthreads();  // the CTA's shares are written
+  if (warp == 0) {
+    const int mine = lane == 0 ? first0 : first1;
+    const int b = __shfl_sync(0xffffffffu, pc.b, mine), gg = __shfl_sync(0xffffffffu, pc.g, mine);
+    const int nt = __shfl_sync(0xffffffffu, pc.nt, mine);
+    const long long seg0 = __shfl_sync(0xffffffffu, pc.seg_start, mine);
+    if (lane < 2) {
+      int done = 0;
+      if (lane == 0 ? cut0 : cut1) {
+        const int c0 = (int)udiv((seg0 + 1) * ctas - 1, total, narrow);
+        const int c1 = (int)udiv((seg0 + nt) * ctas - 1, total, narrow);
+        int* cnt = p.ws_cnt + (size_t)b * Hkv + gg;
+        __threadfence();  // the shares are visible device-wide before they are counted
+        done = atomicAdd(cnt, 1) == c1 - c0;
+        if (done) *cnt = 0;  // nobody else counts here any more: the next call finds zero
+        __threadfence();
       }
-      const int cnt = min(32, c1 - cb + 1);
-      for (int i0 = 0; i0 < cnt; i0 += 8) {  // eight shares' loads in flight
-        float v[8][DPL];
+      done_s[lane] = done;
+    }
+  }
+  __syncthreads();
+  // The CTA that counted last joins: a warp takes W columns of a head, SG shares at a time.
+  constexpr int WPH = NW / G > D / 32 ? D / 32 : (NW / G > 1 ? NW / G : 1);  // warps per head
+  constexpr int W = D / WPH, LPS = W / 4, SG = 32 / LPS, U = 8;
+  for (int which = 0; which < 2; ++which) {
+    if (!done_s[which]) continue;
+    const int first = which ? first1 : first0;
+    const int b = __shfl_sync(0xffffffffu, pc.b, first), gg = __shfl_sync(0xffffffffu, pc.g, first);
+    const int nt = __shfl_sync(0xffffffffu, pc.nt, first);
+    const long long seg0 = __shfl_sync(0xffffffffu, pc.seg_start, first);
+    const int c0 = (int)udiv((seg0 + 1) * ctas - 1, total, narrow), n_sh = (int)udiv((seg0 + nt) * ctas - 1, total, narrow) - c0 + 1;
+    const size_t slot0 = (size_t)b * Hkv + gg + c0;
+    for (int item = warp; item < G * WPH; item += NW) {
+      const int h = item / WPH, col = (item - h * WPH) * W + (lane % LPS) * 4, sg = lane / LPS;
+      const float* rp = p.ws_r + slot0 * G + h;
+      const float* lp = p.ws_l + slot0 * G + h;
+      const float* op = p.ws_o + (slot0 * G + h) * D + col;
+      float4 v[U];  // the first shares' values, asked for before the weights are known
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float* o = p.ws_o + ((seg + min(cb + i0 + i, c1)) * G + h) * D + lane * DPL;
-          if constexpr (DPL == 4) {
-            const float4 f = __ldcg(reinterpret_cast<const float4*>(o));
-            v[i][0] = f.x; v[i][1] = f.y; v[i][2] = f.z; v[i][3] = f.w;
-          } else {
-            const float2 f = __ldcg(reinterpret_cast<const float2*>(o));
-            v[i][0] = f.x; v[i][1] = f.y;
+      for (int u = 0; u < U; ++u)
+        v[u] = __ldcg(reinterpret_cast<const float4*>(op + (size_t)min(u * SG + sg, n_sh - 1) * G * D));
+      float r0 = 0.f, l0 = 0.f, M = -INFINITY;
+      for (int i = lane; i < n_sh; i += 32) {
+        const float li = __ldcg(lp + (size_t)i * G), ri = __ldcg(rp + (size_t)i * G);
+        if (i == lane) r0 = ri, l0 = li;
+        M = fmaxf(M, li > 0.f ? ri + __log2f(li) : -INFINITY);
+      }
+      M = warp_max(M);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      float den = 0.f;
+      for (int base = 0; base < n_sh; base += 32) {
+        const int i = base + lane;
+        float w = 0.f;
+        if (i < n_sh) {
+          const float li = base ? __ldcg(lp + (size_t)i * G) : l0, ri = base ? __ldcg(rp + (size_t)i * G) : r0;
+          w = li > 0.f ? exp2f(ri - M) : 0.f;
+          den = fmaf(w, li, den);
+        }
+        const int cnt = min(32, n_sh - base);
+        for (int i0 = 0; i0 < cnt; i0 += SG * U) {
+          if (base + i0 > 0)
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+              v[u] = __ldcg(reinterpret_cast<const float4*>(op + (size_t)min(base + i0 + u * SG + sg, n_sh - 1) * G * D));
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int at = i0 + u * SG + sg;
+            const float wi = __shfl_sync(0xffffffffu, w, at & 31);
+            if (at < cnt) {
+              acc.x = fmaf(wi, v[u].x, acc.x); acc.y = fmaf(wi, v[u].y, acc.y);
+              acc.z = fmaf(wi, v[u].z, acc.z); acc.w = fmaf(wi, v[u].w, acc.w);
+            }
           }
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float wi = __shfl_sync(0xffffffffu, w2, (i0 + i) & 31);
-          if (i0 + i < cnt)
-#pragma unroll
-            for (int j = 0; j < DPL; ++j) acc[j] = fmaf(wi, v[i][j], acc[j]);
-        }
       }
+      den = warp_sum(den);
+#pragma unroll
+      for (int o = LPS; o < 32; o <<= 1) {
+        acc.x += __shfl_xor_sync(0xffffffffu, acc.x, o); acc.y += __shfl_xor_sync(0xffffffffu, acc.y, o);
+        acc.z += __shfl_xor_sync(0xffffffffu, acc.z, o); acc.w += __shfl_xor_sync(0xffffffffu, acc.w, o);
+      }
+      const size_t at = (size_t)b * p.num_q_heads + (size_t)gg * G + h;
+      if (sg == 0) {
+        const float inv = 1.f / den;
+        uint2 u;
+        u.x = Elt<DT>::from_f2(acc.x * inv, acc.y * inv);
+        u.y = Elt<DT>::from_f2(acc.z * inv, acc.w * inv);
+        *reinterpret_cast<uint2*>(reinterpret_cast<T*>(p.out) + at * D + col) = u;
+      }
+      if (p.lse && lane == 0 && item == h * WPH) p.lse[at] = (M + __log2f(den)) * kLn2;
     }
-    write_out(acc, warp_sum(den2), M2);
   }
 }
 
@@ -878,7 +976,7 @@ bool make_plan(int batch, int Hq, int Hkv, int D, int max_context_len, int num_p
   pl->grid = num_partitions ? num_partitions : (int)std::max<int64_t>(1, std::min<int64_t>(sm_count(), (tiles + 3) / 4));
   auto align256 = [](size_t x) { return (x + 255) & ~size_t(255); };
   const size_t slots = (size_t)batch * Hkv + pl->grid;
-  pl->off_r = align256((size_t)batch * Hq * 4);
+  pl->off_r = align256((size_t)batch * Hkv * 4);
   pl->off_l = pl->off_r + align256(slots * G * 4);
   pl->off_o = pl->off_l + align256(slots * G * 4);
   pl->bytes = pl->off_o + align256(slots * G * D * 4);
@@ -960,6 +1058,7 @@ extern "C" int pa_decode_int4(const void* q, const void* k_codes, const void* v_
   if (num_blocks == 0 && max_context_len > 0) return PA_ERR_INVALID;
   if ((int64_t)num_blocks * block_size >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
   if ((int64_t)max_blocks_per_seq * block_size >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
+  if ((int64_t)num_kv_heads * block_size * head_dim >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
   Plan pl;
   if (!make_plan(batch, num_q_heads, num_kv_heads, head_dim, max_context_len, num_partitions_or_0, &pl))
     return PA_ERR_INVALID;
