@@ -15,8 +15,8 @@
 // What a warp holds of a segment is a piece: a whole segment is written out at once, a partial one goes to
 // shared memory, and after the one barrier at the end of the tiles the pieces of a segment are joined, first
 // within the CTA, then, for the at most two segments that a CTA shares with its neighbours, through the
-// workspace by the CTA that finishes last (a counter per segment, no waiting).  The joining order is the order
-// of the line, so results do not depend on timing.
+// workspace by the warp that counts last (a counter per head, no waiting).  The joining order is the order of
+// the line, so results do not depend on timing.
 //
 // Mathematics.  Products run on mma.m16n8k16 (fp16 in, fp32 out) with tokens (scores) or columns (PV) as the 16
 // rows and up to 8 heads of the group as the 8 columns; G 16 takes two column tiles.
@@ -58,7 +58,7 @@ struct Params {
   const uint8_t* base[4];  // K codes, V codes, K parameters, V parameters
   const int32_t* block_tables;
   const int32_t* context_lens;
-  int* ws_cnt;   // [batch * Hkv] CTAs that have added their share of a segment (zero between calls)
+  int* ws_cnt;   // [batch * Hq] CTAs that have added their share of a head (zero between calls)
   float* ws_r;   // [slots][G] reference R of a share
   float* ws_l;   // [slots][G]
   float* ws_o;   // [slots][G][D]
@@ -66,7 +66,7 @@ struct Params {
   float scale_log2;
 };
 
-enum : int { F_FIRST = 1, F_LAST = 2, F_HEAD = 4, F_TAIL = 8, F_VALID = 16 };
+enum : int { F_VALID = 1, F_HEAD = 2, F_TAIL = 4 };
 
 // A partial piece as the joining step sees it: its segment, whether it holds the segment's first (F_HEAD) and
 // last (F_TAIL) tile, the segment's tiles and where they start on the line.
@@ -85,11 +85,11 @@ struct Layout {
   static constexpr int RING_OFF = 0;
   static constexpr int PART_OFF = RING_OFF + NW * RING;          // the first piece of every warp
   static constexpr int PIECE_OFF = (PART_OFF + NW * PART + 15) / 16 * 16;  // Piece [NW][2]
-  static constexpr int DESC_OFF = PIECE_OFF + NW * 2 * (int)sizeof(Piece);  // int4 [NW][NS]
-  static constexpr int START_OFF = DESC_OFF + NW * NS * 16;      // Start [NW]: where each warp begins
-  static constexpr int SCAN_OFF = START_OFF + NW * 16;           // int64 [NW]
-  static constexpr int DONE_OFF = SCAN_OFF + NW * 8;             // int [2]: segments this CTA joins from the workspace
-  static constexpr int LENS_OFF = DONE_OFF + 8;                  // int [kLens]: lengths, for batches that fit
+  static constexpr int QUEUE_OFF = PIECE_OFF + NW * 2 * (int)sizeof(Piece);  // int4 [NW][NS + 1]: b, KV head, length, tile
+  static constexpr int WIN_OFF = QUEUE_OFF + NW * (NS + 1) * 16;  // uint64 [NW][32]: where the next 32 chunks' codes are
+  static constexpr int SCAN_OFF = WIN_OFF + NW * 256;            // int64 [NW]: tiles of a warp's sequences
+  static constexpr int INCL_OFF = SCAN_OFF + NW * 8;             // int64 [NW * 32]: the scan within the warps
+  static constexpr int LENS_OFF = INCL_OFF + NW * 256;           // int [kLens]: lengths, for batches that fit
   static constexpr int BYTES = LENS_OFF + kLens * 4;
   // Byte offset of word `word` (4 bytes) of row `row` among a tile's codes: 16-byte units of a row are exchanged so
   // that neighbouring rows' units lie in different banks.  Rows 8 apart are exchanged alike.
@@ -97,7 +97,9 @@ struct Layout {
     const int unit = word >> 2;
     return row * ROWB + ((ROWB == 64 ? unit ^ (row >> 1 & 3) : unit ^ (row >> 2 & 1)) << 4) + (word & 3) * 4;
   }
-  static_assert(STAGE % 128 == 0 && sizeof(Piece) % 8 == 0 && PIECE_OFF % 8 == 0, "alignment");
+  static_assert(STAGE % 128 == 0 && sizeof(Piece) % 8 == 0 && PIECE_OFF % 16 == 0 && QUEUE_OFF % 16 == 0 &&
+                    WIN_OFF % 16 == 0,
+                "alignment");
 };
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
@@ -299,7 +301,7 @@ struct State {
     fresh = __any_sync(0xffffffffu, still);
   }
 
-  // One tile in shared memory at `st` (a stage), nv of its 32 tokens valid.
+  // One tile in shared memory at `st` (a stage), its first nv (32 and more: all) tokens valid.
   template <typename LY>
   __device__ __forceinline__ void tile(const uint8_t* st, int nv, int lane) {
     const int g = lane >> 2, c = lane & 3;
@@ -517,178 +519,157 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
   using LY = Layout<D, G, NW, NS>;
   using S = State<DT, D, G>;
   using T = typename Elt<DT>::T;
+  static_assert(NW <= 16, "a warp's lanes hold all pieces of the CTA");
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
-  struct Start {
-    long long pre;  // tiles of all sequences before b, per KV head
-    int b;
-  };
-  Start* starts = reinterpret_cast<Start*>(smem + LY::START_OFF);
-  long long* scan = reinterpret_cast<long long*>(smem + LY::SCAN_OFF);
+  long long* warp_tiles = reinterpret_cast<long long*>(smem + LY::SCAN_OFF);
+  long long* incl_s = reinterpret_cast<long long*>(smem + LY::INCL_OFF);
   Piece* pieces = reinterpret_cast<Piece*>(smem + LY::PIECE_OFF);
+  int* lens_s = reinterpret_cast<int*>(smem + LY::LENS_OFF);
   const int B = p.batch, Hkv = p.num_kv_heads, bs = p.block_size;
   const int cap = p.max_blocks_per_seq * bs;
-
-  int* lens_s = reinterpret_cast<int*>(smem + LY::LENS_OFF);
-  int* done_s = reinterpret_cast<int*>(smem + LY::DONE_OFF);
   if (lane == 0) pieces[2 * warp].flags = pieces[2 * warp + 1].flags = 0;
 
-  // ---- the line: thread i counts the tiles of sequences [i * per, (i + 1) * per); a scan over the threads
+  // ---- the line: thread i counts the tiles of sequences [i * per, (i + 1) * per), a scan within every warp; each warp
+  // then looks its first tile up in the scans
   const int per = (B + NW * 32 - 1) / (NW * 32);
-  const int i0 = min(B, (int)threadIdx.x * per), i1 = min(B, i0 + per);
   auto len_of = [&](int i) { return i < kLens ? lens_s[i] : min(max(__ldg(p.context_lens + i), 0), cap); };
-  long long mine = 0;
-  bool clamped = false;
-  for (int i = i0; i < i1; ++i) {
-    const int L = __ldg(p.context_lens + i);
-    const int Lc = min(max(L, 0), cap);
-    clamped |= L != Lc;
-    if (i < kLens) lens_s[i] = Lc;
-    mine += (Lc + kTile - 1) / kTile;
-  }
-  if (clamped && cta == 0) PA_RECORD_ERROR(PA_ERRBIT_INDEX);
-  long long incl = mine;
+  auto tiles_of = [](int L) { return (L + kTile - 1) / kTile; };
+  {
+    long long incl = 0;
+    bool clamped = false;
+    for (int i = threadIdx.x * per, e = min(B, i + per); i < e; ++i) {
+      const int L = __ldg(p.context_lens + i), Lc = min(max(L, 0), cap);
+      clamped |= L != Lc;
+      if (i < kLens) lens_s[i] = Lc;
+      incl += tiles_of(Lc);
+    }
+    if (clamped && cta == 0) PA_RECORD_ERROR(PA_ERRBIT_INDEX);
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long t = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += t;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    incl_s[threadIdx.x] = incl;
+    if (lane == 31) warp_tiles[warp] = incl;
   }
-  if (lane == 31) scan[warp] = incl;
   __syncthreads();
-  long long before = 0, total = 0;
+  long long wincl = lane < NW ? warp_tiles[lane] : 0;  // tiles up to and with warp `lane`'s sequences
 #pragma unroll
-  for (int w = 0; w < NW; ++w) {
-    if (w < warp) before += scan[w];
-    total += scan[w];
+  for (int o = 1; o < NW; o <<= 1) {
+    const long long t = __shfl_up_sync(0xffffffffu, wincl, o);
+    if (lane >= o) wincl += t;
   }
-  total *= Hkv;
+  const long long total = __shfl_sync(0xffffffffu, wincl, NW - 1) * Hkv;
   const long long ctas = min((long long)gridDim.x, total);  // at least one tile for each CTA that takes part
   const bool narrow = (total + 1) * (ctas + 1) < (1ll << 32);
-  long long x0 = 0, n = 0;
+  long long xs = 0;  // this warp's tiles: [xs, xs + tiles) of the line
+  int tiles = 0;
   if (cta < ctas) {
-    x0 = udiv(total * cta, ctas, narrow);
-    n = udiv(total * (cta + 1), ctas, narrow) - x0;
+    const long long x0 = udiv(total * cta, ctas, narrow), n = udiv(total * (cta + 1), ctas, narrow) - x0;
+    xs = x0 + n * warp / NW;
+    tiles = (int)(x0 + n * (warp + 1) / NW - xs);
   }
-  const long long lo = (before + incl - mine) * Hkv, hi = (before + incl) * Hkv;
-  for (int w = 0; w < NW; ++w) {
-    const long long x = x0 + n * w / NW;
-    if (x < lo || x >= hi) continue;
-    long long pre = before + incl - mine;
-    int i = i0;
-    for (; i < i1; ++i) {
-      const int nt = (len_of(i) + kTile - 1) / kTile;
-      if (x < (pre + nt) * Hkv) break;
-      pre += nt;
-    }
-    starts[w].b = i;
-    starts[w].pre = pre;
-  }
-  __syncthreads();
-
-  // ---- this warp's walk
-  const long long xs = x0 + n * warp / NW;
-  const int tiles = (int)(x0 + n * (warp + 1) / NW - xs);
-  int wb = 0, wg = 0, wL = 0, wnt = 1, wt = 0, left = tiles;  // the next tile to bring in
-  long long wseg = 0;                                         // where its segment starts on the line
-  int win_b = 0, win_len = 0, win_base = 0, win_phys = 0;     // windows of lengths and of block-table entries
-  bool piece_start = true, new_window = true;
+  // the next tile to bring in: tile wt of segment (wb, wg); its piece ends before tile wend, `left` tiles follow it
+  int wb = 0, wg = 0, wL = 0, wt = 0, wend = 0, left = tiles;
+  long long seg_start = 0;  // the consumer's: where its segment starts on the line
   if (tiles > 0) {
-    wb = starts[warp].b;
-    win_b = wb;
-    win_len = wb + lane < B ? len_of(wb + lane) : 0;
-    wL = __shfl_sync(0xffffffffu, win_len, 0);
-    wnt = (wL + kTile - 1) / kTile;
-    const long long in_seq = xs - starts[warp].pre * Hkv;
-    wg = (int)udiv(in_seq, wnt, narrow);
-    wt = (int)(in_seq - (long long)wg * wnt);
-    wseg = xs - wt;
+    const long long y = udiv(xs, Hkv, narrow);  // per KV head
+    const int wsel = __popc(__ballot_sync(0xffffffffu, lane < NW && wincl <= y));
+    const long long before = wsel ? __shfl_sync(0xffffffffu, wincl, wsel - 1) : 0;
+    const long long li = incl_s[wsel * 32 + lane] + before;
+    const int tsel = __popc(__ballot_sync(0xffffffffu, li <= y));
+    long long pre = tsel ? __shfl_sync(0xffffffffu, li, tsel - 1) : before;
+    wb = (wsel * 32 + tsel) * per;
+    for (;; ++wb) {
+      wL = len_of(wb);
+      if (pre + tiles_of(wL) > y) break;
+      pre += tiles_of(wL);
+    }
+    const long long in_seq = xs - pre * Hkv;
+    wg = (int)udiv(in_seq, tiles_of(wL), narrow);
+    wt = (int)(in_seq - (long long)wg * tiles_of(wL));
+    seg_start = xs - wt;
   }
+
+  // ---- what this lane copies of a tile: of each chunk's codes the 16-byte units lane, lane + 32, .. (K and V
+  // alike); of the parameters one unit of the tile's four runs (K chunk 0, K chunk 1, V chunk 0, V chunk 1)
+  constexpr int PER = LY::ROWB / 32, UPR = LY::ROWB / 16, PUNITS = LY::PARB;
+  static_assert(LY::ROWB == 8 * LY::PARB, "offsets of parameters follow from those of codes");
   const uint32_t ring = smem_u32(smem + LY::RING_OFF) + warp * LY::RING;
-  int4* desc = reinterpret_cast<int4*>(smem + LY::DESC_OFF) + warp * NS;
-  const int bs_shift = __ffs(bs) - 1;
-  const uint32_t code_block = Hkv * bs * LY::ROWB, par_block = Hkv * bs * LY::PARB;  // bytes; below 2^31 (host check)
-  // what this lane copies of a 16-token chunk: codes in 16-byte units lane, lane + 32, .. of the chunk's 16 * ROWB
-  // bytes (K and V alike); parameters: one unit of the tile's four runs
-  constexpr int UNITS = LY::ROWB, PER = UNITS / 32 > 0 ? UNITS / 32 : 1;  // code units per chunk, and per lane
-  constexpr int UPR = LY::ROWB / 16, PUNITS = LY::PARB;                   // units per row; parameter units per chunk
-  static_assert(UNITS % 32 == 0, "whole warps copy a chunk's codes");
-  const int par_run = lane / PUNITS, par_unit = lane % PUNITS;            // run: K chunk 0, K chunk 1, V chunk 0, V chunk 1
-  const uint8_t* par_base = p.base[(par_run & 2) ? 3 : 2] + par_unit * 16;
-  const uint32_t par_dst = ((par_run & 2) ? LY::VP_OFF : LY::KP_OFF) + (par_run & 1) * 16 * LY::PARB + par_unit * 16;
+  const uint32_t code_block = Hkv * bs * LY::ROWB;  // bytes; below 2^31 (checked on the host)
+  const uint8_t* kbase = p.base[0] + lane * 16;
+  const uint8_t* vbase = p.base[1] + lane * 16;
+  const int par_run = lane / PUNITS;
+  const uint8_t* par_base = p.base[(par_run & 2) ? 3 : 2] + (lane % PUNITS) * 16;
+  const uint32_t par_dst = ((par_run & 2) ? LY::VP_OFF : LY::KP_OFF) + (par_run & 1) * 16 * LY::PARB + (lane % PUNITS) * 16;
   uint32_t code_dst[PER];
 #pragma unroll
-  for (int e = 0; e < PER; ++e) {
-    const int u = lane + 32 * e;
-    code_dst[e] = LY::code_off(u / UPR, (u % UPR) * 4);
-  }
+  for (int e = 0; e < PER; ++e) code_dst[e] = LY::code_off((lane + 32 * e) / UPR, ((lane + 32 * e) % UPR) * 4);
+  int4* queue = reinterpret_cast<int4*>(smem + LY::QUEUE_OFF) + warp * (NS + 1);  // pieces brought, for the consumer
+  uint64_t* win = reinterpret_cast<uint64_t*>(smem + LY::WIN_OFF) + warp * 32;
+  int win_base = 0, brought = 0;
+  const int bs_shift = __ffs(bs) - 1;
 
-  auto look_up = [&]() {  // block-table entries of the next 32 chunks of the walk's sequence
+  auto look_up = [&]() {  // the next 32 chunks of the walk's segment: where their codes start
     win_base = 2 * wt;
     const int tok = (win_base + lane) * 16;
-    win_phys = tok < wL ? __ldg(p.block_tables + (size_t)wb * p.max_blocks_per_seq + (tok >> bs_shift)) : 0;
-    new_window = false;
-  };
-  auto bring = [&](int s) {  // the walk's next tile into stage s
-    if (new_window || 2 * wt - win_base >= 32 || 2 * wt < win_base) look_up();
-    const int nv = min(kTile, wL - wt * kTile), chunks = nv > 16 ? 2 : 1;
-    const int flags = (piece_start ? F_FIRST : 0) | (wt == wnt - 1 || left == 1 ? F_LAST : 0) |
-                      (wt == 0 ? F_HEAD : 0) | (wt == wnt - 1 ? F_TAIL : 0);
-    if (lane == 0) desc[s] = make_int4(wb, wg, nv | flags << 8, wnt);
-    const uint32_t stage = ring + s * LY::STAGE;
-    const int at = 2 * wt - win_base;
-    int phys = __shfl_sync(0xffffffffu, win_phys, (at + (lane & 1)) & 31);
-    if (phys < 0 || phys >= p.num_blocks) {  // broken caller invariant: record, read block 0 instead
-      if ((lane & 1) < chunks) PA_RECORD_ERROR(PA_ERRBIT_INDEX);
-      phys = 0;
+    uint64_t off = 0;
+    if (tok < wL) {
+      int phys = __ldg(p.block_tables + (size_t)wb * p.max_blocks_per_seq + (tok >> bs_shift));
+      if (phys < 0 || phys >= p.num_blocks) {  // broken caller invariant: record, read block 0 instead
+        PA_RECORD_ERROR(PA_ERRBIT_INDEX);
+        phys = 0;
+      }
+      off = (uint64_t)(uint32_t)phys * code_block + (uint32_t)(wg * bs + (tok & (bs - 1))) * LY::ROWB;
     }
+    __syncwarp();
+    win[lane] = off;
+    __syncwarp();
+  };
+  auto open_piece = [&]() {
+    wend = min(tiles_of(wL), wt + left);
+    left -= wend - wt;
+    if (lane == 0) queue[brought % (NS + 1)] = make_int4(wb, wg, wL, wt);
+    ++brought;
+    look_up();
+  };
+  auto bring = [&](uint32_t stage) {  // the walk's next tile into the stage at this shared address
+    if (2 * wt == win_base + 32) look_up();
+    const ulonglong2 off = *reinterpret_cast<const ulonglong2*>(win + (2 * wt - win_base));
+    const bool two = wL - wt * kTile > 16;
 #pragma unroll
-    for (int ch = 0; ch < 2; ++ch) {
-      if (ch >= chunks) break;
-      const uint32_t ph = __shfl_sync(0xffffffffu, phys, ch);
-      const uint32_t row = wg * bs + ((wt * kTile + 16 * ch) & (bs - 1));
-      const uint64_t off = (uint64_t)ph * code_block + (row * LY::ROWB + lane * 16);
+    for (int e = 0; e < PER; ++e) {
+      cp_async16(stage + LY::K_OFF + code_dst[e], kbase + off.x + 512 * e);
+      cp_async16(stage + LY::V_OFF + code_dst[e], vbase + off.x + 512 * e);
+    }
+    if (two) {
 #pragma unroll
       for (int e = 0; e < PER; ++e) {
-        cp_async16(stage + LY::K_OFF + ch * 16 * LY::ROWB + code_dst[e], p.base[0] + off + 512 * e);
-        cp_async16(stage + LY::V_OFF + ch * 16 * LY::ROWB + code_dst[e], p.base[1] + off + 512 * e);
+        cp_async16(stage + LY::K_OFF + 16 * LY::ROWB + code_dst[e], kbase + off.y + 512 * e);
+        cp_async16(stage + LY::V_OFF + 16 * LY::ROWB + code_dst[e], vbase + off.y + 512 * e);
       }
     }
-    {
-      const uint32_t ph = __shfl_sync(0xffffffffu, phys, par_run & 1);
-      const uint32_t row = wg * bs + ((wt * kTile + 16 * (par_run & 1)) & (bs - 1));
-      if (par_run < 4 && (par_run & 1) < chunks)
-        cp_async16(stage + par_dst, par_base + (uint64_t)ph * par_block + row * LY::PARB);
-    }
-    // step on
-    --left;
-    piece_start = false;
-    if (++wt == wnt && left > 0) {
-      piece_start = true;
-      wseg += wnt;
+    if (par_run < 4 && (two || !(par_run & 1)))
+      cp_async16(stage + par_dst, par_base + (((par_run & 1) ? off.y : off.x) >> 3));
+    if (++wt == wend && left > 0) {  // the next segment; sequences without tokens have no tiles
       wt = 0;
       if (++wg == Hkv) {
         wg = 0;
-        new_window = true;
-        do {  // sequences without tokens have no tiles
-          ++wb;
-          if (wb - win_b >= 32) {
-            win_b = wb;
-            win_len = wb + lane < B ? len_of(wb + lane) : 0;
-          }
-          wL = __shfl_sync(0xffffffffu, win_len, wb - win_b);
-        } while (wL == 0 && wb < B - 1);
-        wnt = (wL + kTile - 1) / kTile;
+        do wL = len_of(++wb);
+        while (wL == 0 && wb < B - 1);
       }
+      open_piece();
     }
   };
-  if (tiles > 0) look_up();
+  if (tiles > 0) open_piece();
 
   // The cache, q and the output may be in use by the preceding kernel (programmatic dependent launch; lengths and
   // block tables are not its outputs): wait for it before the first load of them and before any write.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  long long done_seg = wseg;  // the consumer's segment
+#pragma unroll
   for (int s = 0; s < NS; ++s) {
-    if (left > 0) bring(s);
+    if (s < tiles) bring(ring + s * LY::STAGE);
     cp_async_commit();
   }
   // sequences without a token: zeros, and a log-sum-exp of -inf
@@ -700,42 +681,39 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
       for (int h = lane; h < p.num_q_heads; h += 32) p.lse[(size_t)i * p.num_q_heads + h] = -INFINITY;
   }
 
-  // ---- tiles
+  // ---- pieces and their tiles
   S st;
-  bool head = false;  // the current piece holds its segment's first tile
-  for (int k = 0; k < tiles; ++k) {
-    const int s = k % NS;
-    const int4 d = desc[s];  // written by this warp, before an earlier warp barrier
-    const int flags = d.z >> 8;
-    if (flags & F_FIRST) {  // q is on its way while the tile lands
-      st.begin(reinterpret_cast<const uint8_t*>(p.q) + ((size_t)d.x * p.num_q_heads + (size_t)d.y * G) * D * 2,
-               p.scale_log2, lane);
-      head = flags & F_HEAD;
+  int stage_at = 0;  // byte offset of the current stage
+  for (int k = 0, piece = 0; k < tiles; ++piece) {
+    const int4 d = queue[piece % (NS + 1)];  // written before a warp barrier that this warp has passed
+    const int b = d.x, kvh = d.y, L = d.z, t0 = d.w, nt = tiles_of(L), t1 = min(nt, t0 + tiles - k);
+    // q is on its way while the tile lands
+    st.begin(reinterpret_cast<const uint8_t*>(p.q) + ((size_t)b * p.num_q_heads + (size_t)kvh * G) * D * 2, p.scale_log2,
+             lane);
+    for (int t = t0; t < t1; ++t, ++k) {
+      cp_async_wait<NS - 1>();
+      __syncwarp();
+      st.template tile<LY>(smem + LY::RING_OFF + warp * LY::RING + stage_at, L - t * kTile, lane);
+      __syncwarp();
+      if (k + NS < tiles) bring(ring + stage_at);
+      cp_async_commit();
+      stage_at = stage_at == (NS - 1) * LY::STAGE ? 0 : stage_at + LY::STAGE;
     }
-    cp_async_wait<NS - 1>();
-    __syncwarp();
-    st.template tile<LY>(smem + LY::RING_OFF + warp * LY::RING + s * LY::STAGE, d.z & 0xff, lane);
-    __syncwarp();
-    if (left > 0) bring(s);
-    cp_async_commit();
-    if (!(flags & F_LAST)) continue;
-    // ---- a piece is complete
     st.finish();
-    const bool tail = flags & F_TAIL;
     const int g = lane >> 2, c = lane & 3;
-    if (head && tail) {
-      T* out = reinterpret_cast<T*>(p.out) + ((size_t)d.x * p.num_q_heads + (size_t)d.y * G) * D;
+    if (t0 == 0 && t1 == nt) {
+      T* out = reinterpret_cast<T*>(p.out) + ((size_t)b * p.num_q_heads + (size_t)kvh * G) * D;
 #pragma unroll
-      for (int nt = 0; nt < S::NT; ++nt)
+      for (int n = 0; n < S::NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int h = 8 * nt + 2 * c + e;
+          const int h = 8 * n + 2 * c + e;
           if (h >= G) continue;
-          const float inv = 1.f / st.l[nt][e];
+          const float inv = 1.f / st.l[n][e];
 #pragma unroll
           for (int grp = 0; grp < S::NG; ++grp) {
             float v[8];
-            st.values(nt, grp, e, v);
+            st.values(n, grp, e, v);
             uint4 u;
             u.x = Elt<DT>::from_f2(v[0] * inv, v[1] * inv);
             u.y = Elt<DT>::from_f2(v[2] * inv, v[3] * inv);
@@ -744,48 +722,48 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
             st_v4(out + h * D + 64 * grp + 8 * g, u);
           }
           if (p.lse && g == 0)
-            p.lse[(size_t)d.x * p.num_q_heads + (size_t)d.y * G + h] = (st.R[nt][e] + __log2f(st.l[nt][e])) * kLn2;
+            p.lse[(size_t)b * p.num_q_heads + (size_t)kvh * G + h] = (st.R[n][e] + __log2f(st.l[n][e])) * kLn2;
         }
     } else {
-      const int which = k == tiles - 1;  // the warp's last piece lies in its ring, which is done with
-      float* part = reinterpret_cast<float*>(which ? smem + LY::RING_OFF + warp * LY::RING : smem + LY::PART_OFF + warp * LY::PART);
+      const int which = k == tiles;  // the warp's last piece lies in its ring, which is done with
+      float* part = reinterpret_cast<float*>(which ? smem + LY::RING_OFF + warp * LY::RING
+                                                   : smem + LY::PART_OFF + warp * LY::PART);
 #pragma unroll
-      for (int nt = 0; nt < S::NT; ++nt)
+      for (int n = 0; n < S::NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int h = 8 * nt + 2 * c + e;
+          const int h = 8 * n + 2 * c + e;
           if (h >= G) continue;
 #pragma unroll
           for (int grp = 0; grp < S::NG; ++grp) {
             float v[8];
-            st.values(nt, grp, e, v);
+            st.values(n, grp, e, v);
             float4* o4 = reinterpret_cast<float4*>(part + h * D + 64 * grp + 8 * g);
             o4[0] = make_float4(v[0], v[1], v[2], v[3]);
             o4[1] = make_float4(v[4], v[5], v[6], v[7]);
           }
           if (g == 0) {
-            part[G * D + h] = st.R[nt][e];
-            part[G * D + G + h] = st.l[nt][e];
+            part[G * D + h] = st.R[n][e];
+            part[G * D + G + h] = st.l[n][e];
           }
         }
       if (lane == 0) {
         Piece pc;
-        pc.b = d.x;
-        pc.g = d.y;
-        pc.flags = F_VALID | (head ? F_HEAD : 0) | (tail ? F_TAIL : 0);
-        pc.nt = d.w;
-        pc.seg_start = done_seg;
+        pc.b = b;
+        pc.g = kvh;
+        pc.flags = F_VALID | (t0 == 0 ? F_HEAD : 0) | (t1 == nt ? F_TAIL : 0);
+        pc.nt = nt;
+        pc.seg_start = seg_start;
         pieces[2 * warp + which] = pc;
       }
     }
-    done_seg += d.w;  // empty sequences take no room on the line: the next segment follows at once
+    seg_start += nt;  // empty sequences take no room on the line: the next segment follows at once
   }
   // let the next programmatically launched kernel begin its set-up; it waits for this grid before it touches memory
   asm volatile("griddepcontrol.launch_dependents;");
   __syncthreads();
 
   // ---- join the pieces of each segment.  Lane i holds piece i of the CTA; a run is the pieces of one segment.
-  static_assert(NW <= 16, "a warp's lanes hold all pieces of the CTA");
   Piece pc;
   pc.flags = 0;
   pc.b = pc.g = pc.nt = 0;
@@ -793,6 +771,7 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
   if (lane < 2 * NW) pc = pieces[lane];
   const bool valid = pc.flags & F_VALID;
   const unsigned vmask = __ballot_sync(0xffffffffu, valid);
+  if (vmask == 0) return;
   const unsigned below = vmask & ((1u << lane) - 1u);
   const long long prev = __shfl_sync(0xffffffffu, pc.seg_start, below ? 31 - __clz(below) : lane);
   const unsigned smask = __ballot_sync(0xffffffffu, valid && (!below || prev != pc.seg_start));
@@ -801,30 +780,22 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
     const bool nth = (smask >> lane & 1) && __popc(smask & ((1u << lane) - 1u)) == r;
     return __ffs(__ballot_sync(0xffffffffu, nth)) - 1;
   };
-  auto run_mask = [&](int first) {
-    const unsigned after = first < 31 ? smask & ~((2u << first) - 1u) : 0u;
-    return vmask & ~((1u << first) - 1u) & (after ? (1u << (__ffs(after) - 1)) - 1u : 0xffffffffu);
-  };
-  auto is_whole = [&](int first, unsigned mask) {
-    return (__shfl_sync(0xffffffffu, pc.flags, first) & F_HEAD) &&
-           (__shfl_sync(0xffffffffu, pc.flags, 31 - __clz(mask)) & F_TAIL);
-  };
   auto part_of = [&](int i) {
     return reinterpret_cast<const float*>((i & 1) ? smem + LY::RING_OFF + (i >> 1) * LY::RING
                                                   : smem + LY::PART_OFF + (i >> 1) * LY::PART);
   };
   constexpr int DPL = D / 32;
-  for (int item = warp; item < runs * G; item += NW) {
-    const int r = item / G, h = item - r * G;
-    const int first = run_first(r);
-    const unsigned mask = run_mask(first);
+  // The pieces of run `first` ... joined for head h: reference M (of the pieces' log-sum-exps, so nothing overflows),
+  // sum den and this lane's DPL columns, relative to M.
+  auto join = [&](int first, int h, float& M, float& den, float (&acc)[DPL]) {
+    const unsigned after = first < 31 ? smask & ~((2u << first) - 1u) : 0u;
+    const unsigned mask = vmask & ~((1u << first) - 1u) & (after ? (1u << (__ffs(after) - 1)) - 1u : 0xffffffffu);
     const bool on = mask >> lane & 1;
     const float* part = part_of(on ? lane : first);
     const float R = on ? part[G * D + h] : -INFINITY, l = on ? part[G * D + G + h] : 0.f;
-    const float M = warp_max(l > 0.f ? R + __log2f(l) : -INFINITY);  // of the pieces' log-sum-exps: no overflow below
+    M = warp_max(l > 0.f ? R + __log2f(l) : -INFINITY);
     const float w = l > 0.f ? exp2f(R - M) : 0.f;
-    const float den = warp_sum(w * l);
-    float acc[DPL];
+    den = warp_sum(w * l);
 #pragma unroll
     for (int j = 0; j < DPL; ++j) acc[j] = 0.f;
     for (unsigned m = mask; m; m &= m - 1) {
@@ -834,123 +805,129 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
 #pragma unroll
       for (int j = 0; j < DPL; ++j) acc[j] = fmaf(wi, o[j], acc[j]);
     }
-    const int b = __shfl_sync(0xffffffffu, pc.b, first), gg = __shfl_sync(0xffffffffu, pc.g, first);
-    if (is_whole(first, mask)) {
-      const size_t at = (size_t)b * p.num_q_heads + (size_t)gg * G + h;
-      T* out = reinterpret_cast<T*>(p.out) + at * D + lane * DPL;
-      const float inv = 1.f / den;
+  };
+  // Segments cut between CTAs: the first run if it lacks its segment's first tile or (being the last run, too) its last
+  // tile, and the last run if it lacks its last.
+  const int first0 = run_first(0), first1 = run_first(runs - 1), last = 31 - __clz(vmask);
+  const bool lacks_tail = !(__shfl_sync(0xffffffffu, pc.flags, last) & F_TAIL);
+  const bool cut0 = !(__shfl_sync(0xffffffffu, pc.flags, first0) & F_HEAD) || (runs == 1 && lacks_tail);
+  const bool cut1 = runs > 1 && lacks_tail;
+  const int shared = (cut0 + cut1) * G;  // (segment, head) items of cut segments: the warps take them in turn
+  // 1. this CTA's shares of them, to the workspace: slot segment + CTA (a CTA holds at most one share of a segment,
+  // and neighbouring segments share at most one CTA); then one fence, and all counts at once
+  for (int item = warp; item < shared; item += NW) {
+    const int first = item < G && cut0 ? first0 : first1, h = item % G;
+    float M, den, acc[DPL];
+    join(first, h, M, den, acc);
+    const size_t seg = (size_t)__shfl_sync(0xffffffffu, pc.b, first) * Hkv + __shfl_sync(0xffffffffu, pc.g, first);
+    const size_t row = (seg + cta) * G + h;
 #pragma unroll
-      for (int j = 0; j < DPL / 2; ++j)
-        reinterpret_cast<uint32_t*>(out)[j] = Elt<DT>::from_f2(acc[2 * j] * inv, acc[2 * j + 1] * inv);
-      if (p.lse && lane == 0) p.lse[at] = (M + __log2f(den)) * kLn2;
-    } else {
-      // this CTA's share of a segment cut between CTAs: slot segment + CTA (a CTA holds at most one share of a
-      // segment, and neighbouring segments share at most one CTA)
-      const size_t row = ((size_t)b * Hkv + gg + cta) * G + h;
-#pragma unroll
-      for (int j = 0; j < DPL; ++j) p.ws_o[row * D + lane * DPL + j] = acc[j];
-      if (lane == 0) {
-        p.ws_r[row] = M;
-        p.ws_l[row] = den;
-      }
+    for (int j = 0; j < DPL; ++j) p.ws_o[row * D + lane * DPL + j] = acc[j];
+    if (lane == 0) {
+      p.ws_r[row] = M;
+      p.ws_l[row] = den;
     }
   }
-  if (runs == 0) return;
-  // ---- the segments cut between CTAs: the first and the last run at most
-  const int first0 = run_first(0), first1 = run_first(runs - 1);
-  const bool cut0 = !is_whole(first0, run_mask(first0)), cut1 = runs > 1 && !is_whole(first1, run_mask(first1));
-  if (!cut0 && !cut1) return;
-  __syncthreads();  // the CTA's shares are written
-  if (warp == 0) {
-    const int mine = lane == 0 ? first0 : first1;
-    const int b = __shfl_sync(0xffffffffu, pc.b, mine), gg = __shfl_sync(0xffffffffu, pc.g, mine);
-    const int nt = __shfl_sync(0xffffffffu, pc.nt, mine);
-    const long long seg0 = __shfl_sync(0xffffffffu, pc.seg_start, mine);
-    if (lane < 2) {
-      int done = 0;
-      if (lane == 0 ? cut0 : cut1) {
-        const int c0 = (int)udiv((seg0 + 1) * ctas - 1, total, narrow);
-        const int c1 = (int)udiv((seg0 + nt) * ctas - 1, total, narrow);
-        int* cnt = p.ws_cnt + (size_t)b * Hkv + gg;
-        __threadfence();  // the shares are visible device-wide before they are counted
-        done = atomicAdd(cnt, 1) == c1 - c0;
-        if (done) *cnt = 0;  // nobody else counts here any more: the next call finds zero
-        __threadfence();
-      }
-      done_s[lane] = done;
-    }
-  }
-  __syncthreads();
-  // The CTA that counted last joins: a warp takes W columns of a head, SG shares at a time.
-  constexpr int WPH = NW / G > D / 32 ? D / 32 : (NW / G > 1 ? NW / G : 1);  // warps per head
-  constexpr int W = D / WPH, LPS = W / 4, SG = 32 / LPS, U = 8;
-  for (int which = 0; which < 2; ++which) {
-    if (!done_s[which]) continue;
-    const int first = which ? first1 : first0;
-    const int b = __shfl_sync(0xffffffffu, pc.b, first), gg = __shfl_sync(0xffffffffu, pc.g, first);
+  int done = 0;          // lane i: the warp's item i is complete
+  int c0 = 0, n_sh = 0;  // its first CTA and its number of shares
+  if (warp < shared) {
+    const int item = warp + NW * lane;
+    const int first = item < G && cut0 ? first0 : first1;
+    const int b = __shfl_sync(0xffffffffu, pc.b, first), kvh = __shfl_sync(0xffffffffu, pc.g, first);
     const int nt = __shfl_sync(0xffffffffu, pc.nt, first);
-    const long long seg0 = __shfl_sync(0xffffffffu, pc.seg_start, first);
-    const int c0 = (int)udiv((seg0 + 1) * ctas - 1, total, narrow), n_sh = (int)udiv((seg0 + nt) * ctas - 1, total, narrow) - c0 + 1;
-    const size_t slot0 = (size_t)b * Hkv + gg + c0;
-    for (int item = warp; item < G * WPH; item += NW) {
-      const int h = item / WPH, col = (item - h * WPH) * W + (lane % LPS) * 4, sg = lane / LPS;
-      const float* rp = p.ws_r + slot0 * G + h;
-      const float* lp = p.ws_l + slot0 * G + h;
-      const float* op = p.ws_o + (slot0 * G + h) * D + col;
-      float4 v[U];  // the first shares' values, asked for before the weights are known
+    const long long s0 = __shfl_sync(0xffffffffu, pc.seg_start, first);
+    __threadfence();  // the shares are visible device-wide before they are counted
+    __syncwarp();
+    if (item < shared) {
+      c0 = (int)udiv((s0 + 1) * ctas - 1, total, narrow);
+      n_sh = (int)udiv((s0 + nt) * ctas - 1, total, narrow) - c0 + 1;
+      int* cnt = p.ws_cnt + (size_t)b * p.num_q_heads + (size_t)kvh * G + item % G;
+      done = atomicAdd(cnt, 1) == n_sh - 1;
+      if (done) *cnt = 0;  // nobody else counts here any more: the next call finds zero
+    }
+  }
+  // 2. segments that lie within the CTA
+  const int whole = (runs - cut0 - cut1) * G;
+  for (int item = (warp + NW - shared % NW) % NW; item < whole; item += NW) {
+    const int first = run_first(item / G + cut0), h = item % G;
+    float M, den, acc[DPL];
+    join(first, h, M, den, acc);
+    const size_t at = (size_t)__shfl_sync(0xffffffffu, pc.b, first) * p.num_q_heads +
+                      (size_t)__shfl_sync(0xffffffffu, pc.g, first) * G + h;
+    const float inv = 1.f / den;
+    T* out = reinterpret_cast<T*>(p.out) + at * D + lane * DPL;
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        v[u] = __ldcg(reinterpret_cast<const float4*>(op + (size_t)min(u * SG + sg, n_sh - 1) * G * D));
-      float r0 = 0.f, l0 = 0.f, M = -INFINITY;
-      for (int i = lane; i < n_sh; i += 32) {
-        const float li = __ldcg(lp + (size_t)i * G), ri = __ldcg(rp + (size_t)i * G);
-        if (i == lane) r0 = ri, l0 = li;
-        M = fmaxf(M, li > 0.f ? ri + __log2f(li) : -INFINITY);
+    for (int j = 0; j < DPL / 2; ++j)
+      reinterpret_cast<uint32_t*>(out)[j] = Elt<DT>::from_f2(acc[2 * j] * inv, acc[2 * j + 1] * inv);
+    if (p.lse && lane == 0) p.lse[at] = (M + __log2f(den)) * kLn2;
+  }
+  // 3. the shares of cut segments that this warp counted last, joined: SG shares at a time, 4 columns a lane, U loads
+  // in flight
+  unsigned todo = __ballot_sync(0xffffffffu, done);
+  if (todo) __threadfence();
+  constexpr int LPS = D / 4, SG = 32 / LPS, U = 16 / SG;
+  for (; todo; todo &= todo - 1) {
+    const int j = __ffs(todo) - 1, item = warp + NW * j, h = item % G;
+    const int first = item < G && cut0 ? first0 : first1;
+    const int n = __shfl_sync(0xffffffffu, n_sh, j), from = __shfl_sync(0xffffffffu, c0, j);
+    const int b = __shfl_sync(0xffffffffu, pc.b, first), kvh = __shfl_sync(0xffffffffu, pc.g, first);
+    const size_t row0 = ((size_t)b * Hkv + kvh + from) * G + h;
+    const float* rp = p.ws_r + row0;
+    const float* lp = p.ws_l + row0;
+    const int sg = lane / LPS;
+    const float* op = p.ws_o + row0 * D + (lane % LPS) * 4;
+    float4 v[U];  // the first shares' values, asked for before the weights are known
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u] = __ldcg(reinterpret_cast<const float4*>(op + (size_t)min(u * SG + sg, n - 1) * G * D));
+    float r0 = 0.f, l0 = 0.f, M = -INFINITY;
+    for (int i = lane; i < n; i += 32) {
+      const float li = __ldcg(lp + (size_t)i * G), ri = __ldcg(rp + (size_t)i * G);
+      if (i == lane) r0 = ri, l0 = li;
+      M = fmaxf(M, li > 0.f ? ri + __log2f(li) : -INFINITY);
+    }
+    M = warp_max(M);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float den = 0.f;
+    for (int base = 0; base < n; base += 32) {
+      const int i = base + lane;
+      float w = 0.f;
+      if (i < n) {
+        const float li = base ? __ldcg(lp + (size_t)i * G) : l0, ri = base ? __ldcg(rp + (size_t)i * G) : r0;
+        w = li > 0.f ? exp2f(ri - M) : 0.f;
+        den = fmaf(w, li, den);
       }
-      M = warp_max(M);
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      float den = 0.f;
-      for (int base = 0; base < n_sh; base += 32) {
-        const int i = base + lane;
-        float w = 0.f;
-        if (i < n_sh) {
-          const float li = base ? __ldcg(lp + (size_t)i * G) : l0, ri = base ? __ldcg(rp + (size_t)i * G) : r0;
-          w = li > 0.f ? exp2f(ri - M) : 0.f;
-          den = fmaf(w, li, den);
-        }
-        const int cnt = min(32, n_sh - base);
-        for (int i0 = 0; i0 < cnt; i0 += SG * U) {
-          if (base + i0 > 0)
+      const int cnt = min(32, n - base);
+      for (int i0 = 0; i0 < cnt; i0 += SG * U) {
+        if (base + i0 > 0)
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-              v[u] = __ldcg(reinterpret_cast<const float4*>(op + (size_t)min(base + i0 + u * SG + sg, n_sh - 1) * G * D));
+          for (int u = 0; u < U; ++u)
+            v[u] = __ldcg(reinterpret_cast<const float4*>(op + (size_t)min(base + i0 + u * SG + sg, n - 1) * G * D));
 #pragma unroll
-          for (int u = 0; u < U; ++u) {
-            const int at = i0 + u * SG + sg;
-            const float wi = __shfl_sync(0xffffffffu, w, at & 31);
-            if (at < cnt) {
-              acc.x = fmaf(wi, v[u].x, acc.x); acc.y = fmaf(wi, v[u].y, acc.y);
-              acc.z = fmaf(wi, v[u].z, acc.z); acc.w = fmaf(wi, v[u].w, acc.w);
-            }
+        for (int u = 0; u < U; ++u) {
+          const int at = i0 + u * SG + sg;
+          const float wi = __shfl_sync(0xffffffffu, w, at & 31);
+          if (at < cnt) {
+            acc.x = fmaf(wi, v[u].x, acc.x); acc.y = fmaf(wi, v[u].y, acc.y);
+            acc.z = fmaf(wi, v[u].z, acc.z); acc.w = fmaf(wi, v[u].w, acc.w);
           }
         }
       }
-      den = warp_sum(den);
-#pragma unroll
-      for (int o = LPS; o < 32; o <<= 1) {
-        acc.x += __shfl_xor_sync(0xffffffffu, acc.x, o); acc.y += __shfl_xor_sync(0xffffffffu, acc.y, o);
-        acc.z += __shfl_xor_sync(0xffffffffu, acc.z, o); acc.w += __shfl_xor_sync(0xffffffffu, acc.w, o);
-      }
-      const size_t at = (size_t)b * p.num_q_heads + (size_t)gg * G + h;
-      if (sg == 0) {
-        const float inv = 1.f / den;
-        uint2 u;
-        u.x = Elt<DT>::from_f2(acc.x * inv, acc.y * inv);
-        u.y = Elt<DT>::from_f2(acc.z * inv, acc.w * inv);
-        *reinterpret_cast<uint2*>(reinterpret_cast<T*>(p.out) + at * D + col) = u;
-      }
-      if (p.lse && lane == 0 && item == h * WPH) p.lse[at] = (M + __log2f(den)) * kLn2;
     }
+    den = warp_sum(den);
+#pragma unroll
+    for (int o = LPS; o < 32; o <<= 1) {
+      acc.x += __shfl_xor_sync(0xffffffffu, acc.x, o); acc.y += __shfl_xor_sync(0xffffffffu, acc.y, o);
+      acc.z += __shfl_xor_sync(0xffffffffu, acc.z, o); acc.w += __shfl_xor_sync(0xffffffffu, acc.w, o);
+    }
+    const size_t at = (size_t)b * p.num_q_heads + (size_t)kvh * G + h;
+    if (sg == 0) {
+      const float inv = 1.f / den;
+      uint2 u;
+      u.x = Elt<DT>::from_f2(acc.x * inv, acc.y * inv);
+      u.y = Elt<DT>::from_f2(acc.z * inv, acc.w * inv);
+      *reinterpret_cast<uint2*>(reinterpret_cast<T*>(p.out) + at * D + lane * 4) = u;
+    }
+    if (p.lse && lane == 0) p.lse[at] = (M + __log2f(den)) * kLn2;
   }
 }
 
@@ -976,7 +953,7 @@ bool make_plan(int batch, int Hq, int Hkv, int D, int max_context_len, int num_p
   pl->grid = num_partitions ? num_partitions : (int)std::max<int64_t>(1, std::min<int64_t>(sm_count(), (tiles + 3) / 4));
   auto align256 = [](size_t x) { return (x + 255) & ~size_t(255); };
   const size_t slots = (size_t)batch * Hkv + pl->grid;
-  pl->off_r = align256((size_t)batch * Hkv * 4);
+  pl->off_r = align256((size_t)batch * Hq * 4);
   pl->off_l = pl->off_r + align256(slots * G * 4);
   pl->off_o = pl->off_l + align256(slots * G * 4);
   pl->bytes = pl->off_o + align256(slots * G * D * 4);

@@ -425,7 +425,7 @@ def test_decode_int4_graph_replay_and_side_stream():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
-        counters = 4 * 5 * 8
+        counters = 4 * 5 * 16
         assert (ws[:counters] == 0).all()
 
 
