@@ -24,10 +24,13 @@
 //     code * 2^-20, exactly.  Widening a word of 8 codes is one shift and four ANDs, with no offset to take out
 //     again; the factors 2^24 and 16 sit in the score scale, in q (its odd values enter divided by 16) and in
 //     the final scaling of the output rows.
-//   * Scores: s_t = sum_group s_K (sum code q + z_K sum q); the group sums of q come from a product with codes 1.
-//   * PV: the weight of a token enters times its V scale, P' = 2^(x - R) s_V in fp16 (rounded once, 2^-11; its
-//     rounded value also multiplies the zero point, so code and zero-point parts carry the same rounding and
-//     the error stays relative to the value, not to the code):  O += P' code,  Z += P' z_V (fp32).
+//   * Parameters are converted once per token (lane = token), not once per lane that needs them, and handed round
+//     through shared memory: s_K times the score scale as fp32, s_V as fp32, both z as fp16.
+//   * Scores: s_t = sum_group s_K (sum code q + z_K sum q).  The zero-point part is one more product per group, of z
+//     (times 2^-6: below 2^-8 it loses bits worth 2^-19 of a code) with the group sum of q in two fp16 terms.
+//   * PV: the weight of a token enters times its V scale, P' = 2^(x - R) s_V in fp16 (rounded once, 2^-11).  The
+//     zero-point part is again one product per group, of z_V with the same P', so code and zero-point parts carry
+//     the same rounding and the error stays relative to the value, not to the code.
 //   * Online softmax with a reference R per head that moves only when it must: a piece starts with a guess, which
 //     stays if it puts the first tile's largest P' into [2^3, 2^15) and is set so (to (2^3, 2^4]) otherwise; later R
 //     is raised only when P' come near 2^15 or the sum l passes 2^100.  Any R gives the same quotient O / l;
@@ -46,7 +49,7 @@ namespace {
 using namespace pa;
 
 constexpr int kTile = 32;            // tokens per tile: two 16-token chunks, each within one block
-constexpr int kLens = 1024;           // sequences whose lengths a CTA keeps in shared memory
+constexpr int kLens = 512;            // sequences whose lengths a CTA keeps in shared memory
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGuess = -8.f;       // a piece's first reference: fits when its largest weight * V scale is 2^-5 .. 2^7
 constexpr float kUnit = 16777216.f;  // 2^24: what a code's fp16 subnormal stands for, inverted
@@ -55,7 +58,10 @@ struct Params {
   const void* q;
   void* out;
   float* lse;
-  const uint8_t* base[4];  // K codes, V codes, K parameters, V parameters
+  const uint8_t* k_codes;
+  const uint8_t* k_params;
+  long long v_codes;  // where V's codes and parameters lie, relative to K's (an address less in registers)
+  long long v_params;
   const int32_t* block_tables;
   const int32_t* context_lens;
   int* ws_cnt;   // [batch * Hq] CTAs that have added their share of a head (zero between calls)
@@ -75,6 +81,21 @@ struct Piece {
   long long seg_start;
 };
 
+// A piece on its way: filed by the walk that brings tiles in, taken up by the consumer.
+struct Queued {
+  int b, g, L, t0;      // sequence, KV head, length, first tile
+  long long seg_start;  // where the segment starts on the line
+  long long pad;
+};
+// The walk of a warp between two windows of block lookups (kept in shared memory: it is looked at once in 16 tiles).
+struct Walk {
+  int b, g, L, t;       // segment, its length, next tile
+  int end, left;        // where the piece ends, and the tiles that follow it
+  int filed, pad;       // pieces filed
+  long long seg_start;
+  long long pad2;
+};
+
 template <int D, int G, int NW, int NS>
 struct Layout {
   static constexpr int NG = D / 64, ROWB = D / 2, PARB = NG * 4;
@@ -83,13 +104,17 @@ struct Layout {
   static constexpr int PART = (G * (D + 2) * 4 + 15) / 16 * 16;  // a partial piece: o [G][D], R [G], l [G]
   static constexpr int RING = NS * STAGE > PART ? NS * STAGE : (PART + 127) / 128 * 128;  // also the last piece
   static constexpr int RING_OFF = 0;
+  static constexpr int SV_OFF = 0, Z_OFF = kTile * NG * 4, CONV = Z_OFF + kTile * NG * 2;  // a warp's converted V parameters
   static constexpr int PART_OFF = RING_OFF + NW * RING;          // the first piece of every warp
   static constexpr int PIECE_OFF = (PART_OFF + NW * PART + 15) / 16 * 16;  // Piece [NW][2]
-  static constexpr int QUEUE_OFF = PIECE_OFF + NW * 2 * (int)sizeof(Piece);  // int4 [NW][NS + 1]: b, KV head, length, tile
-  static constexpr int WIN_OFF = QUEUE_OFF + NW * (NS + 1) * 16;  // uint64 [NW][32]: where the next 32 chunks' codes are
+  static constexpr int NQ = NS + 2;                              // pieces filed and not done: NS stages' and one more
+  static constexpr int QUEUE_OFF = PIECE_OFF + NW * 2 * (int)sizeof(Piece);  // Queued [NW][NQ]
+  static constexpr int WALK_OFF = QUEUE_OFF + NW * NQ * (int)sizeof(Queued);  // Walk [NW]
+  static constexpr int WIN_OFF = WALK_OFF + NW * (int)sizeof(Walk);  // uint64 [NW][32]: where the next 32 chunks' codes are
   static constexpr int SCAN_OFF = WIN_OFF + NW * 256;            // int64 [NW]: tiles of a warp's sequences
-  static constexpr int INCL_OFF = SCAN_OFF + NW * 8;             // int64 [NW * 32]: the scan within the warps
-  static constexpr int LENS_OFF = INCL_OFF + NW * 256;           // int [kLens]: lengths, for batches that fit
+  static constexpr int INCL_OFF = WIN_OFF;                       // int64 [NW * 32]: the scan within the warps, at the start
+  static constexpr int CONV_OFF = SCAN_OFF + NW * 8;             // CONV [NW]
+  static constexpr int LENS_OFF = CONV_OFF + NW * CONV;          // int [kLens]: lengths, for batches that fit
   static constexpr int BYTES = LENS_OFF + kLens * 4;
   // Byte offset of word `word` (4 bytes) of row `row` among a tile's codes: 16-byte units of a row are exchanged so
   // that neighbouring rows' units lie in different banks.  Rows 8 apart are exchanged alike.
@@ -97,8 +122,8 @@ struct Layout {
     const int unit = word >> 2;
     return row * ROWB + ((ROWB == 64 ? unit ^ (row >> 1 & 3) : unit ^ (row >> 2 & 1)) << 4) + (word & 3) * 4;
   }
-  static_assert(STAGE % 128 == 0 && sizeof(Piece) % 8 == 0 && PIECE_OFF % 16 == 0 && QUEUE_OFF % 16 == 0 &&
-                    WIN_OFF % 16 == 0,
+  static_assert(STAGE % 128 == 0 && sizeof(Piece) % 8 == 0 && sizeof(Queued) == 32 && sizeof(Walk) == 48 && PIECE_OFF % 16 == 0 && QUEUE_OFF % 16 == 0 &&
+                    WIN_OFF % 16 == 0 && CONV_OFF % 16 == 0 && CONV % 16 == 0,
                 "alignment");
 };
 
@@ -173,9 +198,9 @@ template <int DT, int D, int G>
 struct State {
   static constexpr int NG = D / 64, KS = D / 16, NT = (G + 7) / 8, WPL = D / 32;  // WPL: K words a lane reads of a row
   uint32_t qb[NT][KS][2];  // q as B operand (fp16, prescaled; odd values divided by 16)
-  float qsum[NT][NG][2];   // sum of q over a group times 2^-24, heads 8nt + 2c + {0,1}
+  uint32_t qsum[NT][NG];   // B operand of the zero-point product: lanes c = 0 the sum of q over a group, 2^-18 of it in two terms
   float o[NT][KS][4];      // O^T times 2^-24 (rows g) and 2^-20 (rows g + 8), columns heads
-  float z[NT][NG][2];      // this lane's part of sum P' z_V
+  float z[NT][NG][4];      // sum P' z_V (columns heads; all rows alike)
   float l[NT][2];          // this lane's part of sum 2^(x - R)
   float R[NT][2];
   float qs;                // scale * log2(e) * 2^24 / prescale
@@ -244,9 +269,11 @@ struct State {
           for (int s = 0; s < 2; ++s)
             mma_f16(i == grp && s == 0, acc, 0x00010001u, 0x00010001u, 0x00100010u, 0x00100010u, qb[nt][2 * i + s][0],
                     qb[nt][2 * i + s][1]);
-        qsum[nt][grp][0] = acc[0];
-        qsum[nt][grp][1] = acc[1];
-        z[nt][grp][0] = z[nt][grp][1] = 0.f;
+        // lane g takes head 8nt + g, which column 2 (g / 2) + g % 2 of any row holds; acc is 2^-24 of the sum
+        const float s0 = __shfl_sync(0xffffffffu, acc[0], g >> 1), s1 = __shfl_sync(0xffffffffu, acc[1], g >> 1);
+        const float sum = ((g & 1) ? s1 : s0) * 64.f, hi = __half2float(__float2half_rn(sum));
+        qsum[nt][grp] = c == 0 ? pack_h2(hi, sum - hi) : 0u;
+        z[nt][grp][0] = z[nt][grp][1] = z[nt][grp][2] = z[nt][grp][3] = 0.f;
       }
 #pragma unroll
       for (int i = 0; i < KS; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
@@ -292,7 +319,7 @@ struct State {
 #pragma unroll
           for (int i = 0; i < KS; ++i) o[nt][i][e] *= f, o[nt][i][2 + e] *= f;
 #pragma unroll
-          for (int grp = 0; grp < NG; ++grp) z[nt][grp][e] *= f;
+          for (int grp = 0; grp < NG; ++grp) z[nt][grp][e] *= f, z[nt][grp][2 + e] *= f;
         }
         R[nt][e] += up;
 #pragma unroll
@@ -301,141 +328,169 @@ struct State {
     fresh = __any_sync(0xffffffffu, still);
   }
 
-  // One tile in shared memory at `st` (a stage), its first nv (32 and more: all) tokens valid.
+  // One tile in shared memory at `st` (a stage), its first nv (32 and more: all) tokens valid; conv: the warp's room for
+  // converted V parameters (those of K replace the stage's).
   template <typename LY>
-  __device__ __forceinline__ void tile(const uint8_t* st, int nv, int lane) {
+  __device__ __forceinline__ void tile(uint8_t* st, uint8_t* conv, int nv, int lane) {
     const int g = lane >> 2, c = lane & 3;
-    // ---- scores: rows tokens g, g + 8, g + 16, g + 24 (r = 2 mt + hh), columns heads 8nt + 2c + {0,1}
-    const uint8_t* kl = st + LY::K_OFF + LY::code_off(g, WPL * c);
-    const uint8_t* kpl = st + LY::KP_OFF + g * LY::PARB;
-    const uint8_t* vpl = st + LY::VP_OFF + g * LY::PARB;
+    // ---- parameters of token `lane`
+    uint32_t kw[NG], vw[NG];
+    if constexpr (NG == 2) {
+      const uint2 a = *reinterpret_cast<const uint2*>(st + LY::KP_OFF + lane * 8);
+      const uint2 b = *reinterpret_cast<const uint2*>(st + LY::VP_OFF + lane * 8);
+      kw[0] = a.x; kw[1] = a.y;
+      vw[0] = b.x; vw[1] = b.y;
+    } else {
+      kw[0] = *reinterpret_cast<const uint32_t*>(st + LY::KP_OFF + lane * 4);
+      vw[0] = *reinterpret_cast<const uint32_t*>(st + LY::VP_OFF + lane * 4);
+    }
+    // ---- K codes: rows tokens g, g + 8, g + 16, g + 24 (r = 2 mt + hh)
+    uint32_t kc[4][WPL];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const uint8_t* a = st + LY::K_OFF + LY::code_off(g, WPL * c) + 8 * r * LY::ROWB;
+      if constexpr (WPL == 4) {
+        const uint4 u = *reinterpret_cast<const uint4*>(a);
+        kc[r][0] = u.x; kc[r][1] = u.y; kc[r][2] = u.z; kc[r][3] = u.w;
+      } else {
+        const uint2 u = *reinterpret_cast<const uint2*>(a);
+        kc[r][0] = u.x; kc[r][1] = u.y;
+      }
+    }
+    __syncwarp();  // every lane holds its parameters: their place may be overwritten
+    float vs[NG];
+    {
+      float ks[NG], kz[NG], vz[NG];
+#pragma unroll
+      for (int grp = 0; grp < NG; ++grp) {
+        const float2 a = Elt<DT>::to_f2(kw[grp]), b = Elt<DT>::to_f2(vw[grp]);
+        ks[grp] = a.x * qs;
+        kz[grp] = a.y * 0.015625f;
+        vs[grp] = lane < nv ? b.x : 0.f;  // rows past the end hold anything, NaN among it
+        vz[grp] = lane < nv ? b.y : 0.f;
+      }
+      __half* z = reinterpret_cast<__half*>(conv + LY::Z_OFF) + (lane >> 1) * 2 * NG + (lane & 1);
+      if constexpr (NG == 2) {
+        *reinterpret_cast<uint4*>(st + LY::KP_OFF + lane * 16) = make_uint4(
+            __float_as_uint(ks[0]), __float_as_uint(ks[1]), pack_h2(kz[0], kz[0]), pack_h2(kz[1], kz[1]));
+        *reinterpret_cast<float2*>(conv + LY::SV_OFF + lane * 8) = make_float2(vs[0], vs[1]);
+        const __half2 zz = __floats2half2_rn(vz[0], vz[1]);
+        z[0] = __low2half(zz);
+        z[2] = __high2half(zz);
+      } else {
+        *reinterpret_cast<uint2*>(st + LY::KP_OFF + lane * 8) = make_uint2(__float_as_uint(ks[0]), pack_h2(kz[0], kz[0]));
+        *reinterpret_cast<float*>(conv + LY::SV_OFF + lane * 4) = vs[0];
+        z[0] = __float2half_rn(vz[0]);
+      }
+    }
+    // the tile's largest V scale (not negative: its bits order as its value does)
+    const float sv_top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(NG == 2 ? fmaxf(vs[0], vs[NG - 1]) : vs[0])));
+    __syncwarp();
+    // ---- scores relative to R, columns heads 8nt + 2c + {0,1}
     float x[2][NT][4];
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt) {
-      const uint8_t* ra = kl + 16 * mt * LY::ROWB;
-      const uint8_t* rb = ra + 8 * LY::ROWB;
-      uint32_t wa[WPL], wb[WPL];
-      if constexpr (WPL == 4) {
-        const uint4 a = *reinterpret_cast<const uint4*>(ra), b = *reinterpret_cast<const uint4*>(rb);
-        wa[0] = a.x; wa[1] = a.y; wa[2] = a.z; wa[3] = a.w;
-        wb[0] = b.x; wb[1] = b.y; wb[2] = b.z; wb[3] = b.w;
-      } else {
-        const uint2 a = *reinterpret_cast<const uint2*>(ra), b = *reinterpret_cast<const uint2*>(rb);
-        wa[0] = a.x; wa[1] = a.y;
-        wb[0] = b.x; wb[1] = b.y;
+      float ks[2][NG];
+      uint32_t kz[2][NG];
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        const uint8_t* a = st + LY::KP_OFF + (16 * mt + 8 * hh + g) * 8 * NG;
+        if constexpr (NG == 2) {
+          const uint4 u = *reinterpret_cast<const uint4*>(a);
+          ks[hh][0] = __uint_as_float(u.x); ks[hh][1] = __uint_as_float(u.y);
+          kz[hh][0] = u.z; kz[hh][1] = u.w;
+        } else {
+          const uint2 u = *reinterpret_cast<const uint2*>(a);
+          ks[hh][0] = __uint_as_float(u.x);
+          kz[hh][0] = u.y;
+        }
       }
       float acc[NT][NG][4];
 #pragma unroll
       for (int i = 0; i < WPL; ++i)
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          const uint32_t a = wa[i] >> (8 * s), b = wb[i] >> (8 * s);
+          const uint32_t a = kc[2 * mt][i] >> (8 * s), b = kc[2 * mt + 1][i] >> (8 * s);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
             mma_f16(i < NG && s == 0, acc[nt][i % NG], a & kLow, b & kLow, a & kHigh, b & kHigh, qb[nt][2 * i + s][0],
                     qb[nt][2 * i + s][1]);
         }
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        const uint8_t* pa = kpl + (16 * mt + 8 * hh) * LY::PARB;
-        float2 par[NG];
-        if constexpr (NG == 2) {
-          const uint2 w = *reinterpret_cast<const uint2*>(pa);
-          par[0] = Elt<DT>::to_f2(w.x);
-          par[1] = Elt<DT>::to_f2(w.y);
-        } else {
-          par[0] = Elt<DT>::to_f2(*reinterpret_cast<const uint32_t*>(pa));
-        }
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int grp = 0; grp < NG; ++grp) {
-          const float sq = par[grp].x * qs;
+          mma_f16(acc[nt][grp], kz[0][grp], kz[1][grp], kz[0][grp], kz[1][grp], qsum[nt][grp], 0u);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              x[mt][nt][2 * hh + e] = fmaf(fmaf(par[grp].y, qsum[nt][grp][e], acc[nt][grp][2 * hh + e]), sq,
-                                           grp == 0 ? -R[nt][e] : x[mt][nt][2 * hh + e]);
+          for (int e = 0; e < 4; ++e)
+            x[mt][nt][e] = fmaf(acc[nt][grp][e], ks[e >> 1][grp], grp == 0 ? -R[nt][e & 1] : x[mt][nt][e]);
         }
-      }
     }
-    // ---- V parameters of the same rows
-    float sv[4][NG], zv[4][NG];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const uint8_t* pa = vpl + 8 * r * LY::PARB;
-      uint32_t w[NG];
-      if constexpr (NG == 2) {
-        const uint2 u = *reinterpret_cast<const uint2*>(pa);
-        w[0] = u.x;
-        w[1] = u.y;
-      } else {
-        w[0] = *reinterpret_cast<const uint32_t*>(pa);
-      }
-#pragma unroll
-      for (int grp = 0; grp < NG; ++grp) {
-        const float2 f = Elt<DT>::to_f2(w[grp]);
-        sv[r][grp] = f.x;
-        zv[r][grp] = f.y;
-      }
-    }
-    if (nv < kTile) {  // rows past the end hold anything, NaN among it
+    if (nv < kTile) {
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        if (8 * r + g >= nv) {
-#pragma unroll
-          for (int grp = 0; grp < NG; ++grp) sv[r][grp] = zv[r][grp] = 0.f;
+        if (8 * r + g >= nv)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) x[r >> 1][nt][2 * (r & 1)] = x[r >> 1][nt][2 * (r & 1) + 1] = -INFINITY;
-        }
     }
-    // ---- weights; taken again after a move of the references
+    // ---- weights; taken once more after a move of the references
+    float sv[4][NG];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float* a = reinterpret_cast<const float*>(conv + LY::SV_OFF) + (8 * r + g) * NG;
+      if constexpr (NG == 2) {
+        const float2 u = *reinterpret_cast<const float2*>(a);
+        sv[r][0] = u.x;
+        sv[r][1] = u.y;
+      } else {
+        sv[r][0] = a[0];
+      }
+    }
     uint32_t pk[NT][NG][4];
     float sum[NT][2];
-    auto weights = [&]() -> bool {
-      __half2 all = as_h2(0u);  // the sum of all P', at least each of them
-      bool over = false;
+    for (bool moved = false;; moved = true) {
+      bool move = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        sum[nt][0] = l[nt][0];
-        sum[nt][1] = l[nt][1];
+        sum[nt][0] = sum[nt][1] = 0.f;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const float p0 = fast_exp2(x[r >> 1][nt][2 * (r & 1)]), p1 = fast_exp2(x[r >> 1][nt][2 * (r & 1) + 1]);
           sum[nt][0] += p0;
           sum[nt][1] += p1;
 #pragma unroll
-          for (int grp = 0; grp < NG; ++grp) {
-            pk[nt][grp][r] = pack_h2(p0 * sv[r][grp], p1 * sv[r][grp]);
-            all = __hadd2(all, as_h2(pk[nt][grp][r]));
-          }
+          for (int grp = 0; grp < NG; ++grp) pk[nt][grp][r] = pack_h2(p0 * sv[r][grp], p1 * sv[r][grp]);
         }
-        over |= !(sum[nt][0] < 1.2676506e30f) || !(sum[nt][1] < 1.2676506e30f);  // 2^100
+        // each P' is at most the lane's sum times the largest scale: below 2^15, and l below 2^100
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          move |= !(sum[nt][e] * sv_top < 32768.f);
+          sum[nt][e] += l[nt][e];
+          move |= !(sum[nt][e] < 1.2676506e30f);
+        }
       }
-      return over || ((as_u32(all) + 0x08000800u) & 0x80008000u) != 0;  // 2^15 or more (exponent bits 1111x)
-    };
-    bool move = __any_sync(0xffffffffu, weights());
-    if (fresh && !move) {  // is the guess large enough for every head?
-      bool low = false;
+      move = __any_sync(0xffffffffu, move);
+      if (fresh && !move) {  // is the guess large enough for every head?
+        bool low = false;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        __half2 top = as_h2(0u);
+        for (int nt = 0; nt < NT; ++nt) {
+          __half2 top = as_h2(0u);
 #pragma unroll
-        for (int grp = 0; grp < NG; ++grp)
+          for (int grp = 0; grp < NG; ++grp)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) top = __hmax2(top, as_h2(pk[nt][grp][r]));
+            for (int r = 0; r < 4; ++r) top = __hmax2(top, as_h2(pk[nt][grp][r]));
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) top = __hmax2(top, as_h2(__shfl_xor_sync(0xffffffffu, as_u32(top), o)));
-        low |= !(__low2float(top) >= 8.f) || !(__high2float(top) >= 8.f);
+          for (int o = 4; o < 32; o <<= 1) top = __hmax2(top, as_h2(__shfl_xor_sync(0xffffffffu, as_u32(top), o)));
+          low |= !(__low2float(top) >= 8.f) || !(__high2float(top) >= 8.f);
+        }
+        move = __any_sync(0xffffffffu, low);
+        fresh = move;
       }
-      move = __any_sync(0xffffffffu, low);
-      fresh = move;
-    }
-    if (move) {
+      if (!move || moved) break;
       float svm[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) svm[r] = NG == 2 ? fmaxf(sv[r][0], sv[r][NG - 1]) : sv[r][0];
       rebase(x, svm);
-      weights();
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -444,12 +499,7 @@ struct State {
 #pragma unroll
       for (int grp = 0; grp < NG; ++grp)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float2 p = __half22float2(as_h2(pk[nt][grp][r]));
-          z[nt][grp][0] = fmaf(p.x, zv[r][grp], z[nt][grp][0]);
-          z[nt][grp][1] = fmaf(p.y, zv[r][grp], z[nt][grp][1]);
-          pk[nt][grp][r] = trans8x8(pk[nt][grp][r]);  // tokens along the rows of the B operand
-        }
+        for (int r = 0; r < 4; ++r) pk[nt][grp][r] = trans8x8(pk[nt][grp][r]);  // tokens along the rows of the B operand
     }
     // ---- O^T += V^T P'^T: tokens 2c, 2c + 1, 2c + 8, 2c + 9 of each half; word `grp` of lane g's piece of a row holds
     // values 64 grp + 8 g ..
@@ -474,6 +524,18 @@ struct State {
           w[t][0] = *reinterpret_cast<const uint32_t*>(a);
         }
       }
+      uint32_t zp[2][NG];  // z of tokens 2c, 2c + 1 and of 2c + 8, 2c + 9
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        const uint32_t* a = reinterpret_cast<const uint32_t*>(conv + LY::Z_OFF) + ((2 * mt + hh) * 4 + c) * NG;
+#pragma unroll
+        for (int grp = 0; grp < NG; ++grp) zp[hh][grp] = a[grp];
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int grp = 0; grp < NG; ++grp)
+          mma_f16(z[nt][grp], zp[0][grp], zp[0][grp], zp[1][grp], zp[1][grp], pk[nt][grp][2 * mt], pk[nt][grp][2 * mt + 1]);
 #pragma unroll
       for (int grp = 0; grp < NG; ++grp)
 #pragma unroll
@@ -492,16 +554,12 @@ struct State {
     }
   }
 
-  // Completes the lanes' parts; after it l is the sum and z the zero-point part for every lane of a column.
+  // Completes the lanes' parts of l.
   __device__ __forceinline__ void finish() {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        l[nt][e] = rows_sum(l[nt][e]);
-#pragma unroll
-        for (int grp = 0; grp < NG; ++grp) z[nt][grp][e] = rows_sum(z[nt][grp][e]);
-      }
+      for (int e = 0; e < 2; ++e) l[nt][e] = rows_sum(l[nt][e]);
   }
   // The 8 output values 64 grp + 8 g .. of head 8nt + 2c + e, relative to R.
   __device__ __forceinline__ void values(int nt, int grp, int e, float (&v)[8]) const {
@@ -570,9 +628,7 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
     xs = x0 + n * warp / NW;
     tiles = (int)(x0 + n * (warp + 1) / NW - xs);
   }
-  // the next tile to bring in: tile wt of segment (wb, wg); its piece ends before tile wend, `left` tiles follow it
-  int wb = 0, wg = 0, wL = 0, wt = 0, wend = 0, left = tiles;
-  long long seg_start = 0;  // the consumer's: where its segment starts on the line
+  Walk w0 = {};
   if (tiles > 0) {
     const long long y = udiv(xs, Hkv, narrow);  // per KV head
     const int wsel = __popc(__ballot_sync(0xffffffffu, lane < NW && wincl <= y));
@@ -580,96 +636,118 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
     const long long li = incl_s[wsel * 32 + lane] + before;
     const int tsel = __popc(__ballot_sync(0xffffffffu, li <= y));
     long long pre = tsel ? __shfl_sync(0xffffffffu, li, tsel - 1) : before;
-    wb = (wsel * 32 + tsel) * per;
-    for (;; ++wb) {
-      wL = len_of(wb);
-      if (pre + tiles_of(wL) > y) break;
-      pre += tiles_of(wL);
+    w0.b = (wsel * 32 + tsel) * per;
+    for (;; ++w0.b) {
+      w0.L = len_of(w0.b);
+      if (pre + tiles_of(w0.L) > y) break;
+      pre += tiles_of(w0.L);
     }
     const long long in_seq = xs - pre * Hkv;
-    wg = (int)udiv(in_seq, tiles_of(wL), narrow);
-    wt = (int)(in_seq - (long long)wg * tiles_of(wL));
-    seg_start = xs - wt;
+    w0.g = (int)udiv(in_seq, tiles_of(w0.L), narrow);
+    w0.t = (int)(in_seq - (long long)w0.g * tiles_of(w0.L));
+    w0.seg_start = xs - w0.t;
   }
+  __syncthreads();  // the scans are done with: the windows take their place
 
   // ---- what this lane copies of a tile: of each chunk's codes the 16-byte units lane, lane + 32, .. (K and V
   // alike); of the parameters one unit of the tile's four runs (K chunk 0, K chunk 1, V chunk 0, V chunk 1)
   constexpr int PER = LY::ROWB / 32, UPR = LY::ROWB / 16, PUNITS = LY::PARB;
   static_assert(LY::ROWB == 8 * LY::PARB, "offsets of parameters follow from those of codes");
   const uint32_t ring = smem_u32(smem + LY::RING_OFF) + warp * LY::RING;
-  const uint32_t code_block = Hkv * bs * LY::ROWB;  // bytes; below 2^31 (checked on the host)
-  const uint8_t* kbase = p.base[0] + lane * 16;
-  const uint8_t* vbase = p.base[1] + lane * 16;
   const int par_run = lane / PUNITS;
-  const uint8_t* par_base = p.base[(par_run & 2) ? 3 : 2] + (lane % PUNITS) * 16;
+  const uint8_t* kbase = p.k_codes + lane * 16;
+  const uint8_t* par_base = p.k_params + ((par_run & 2) ? p.v_params : 0) + (lane % PUNITS) * 16;
   const uint32_t par_dst = ((par_run & 2) ? LY::VP_OFF : LY::KP_OFF) + (par_run & 1) * 16 * LY::PARB + (lane % PUNITS) * 16;
   uint32_t code_dst[PER];
 #pragma unroll
   for (int e = 0; e < PER; ++e) code_dst[e] = LY::code_off((lane + 32 * e) / UPR, ((lane + 32 * e) % UPR) * 4);
-  int4* queue = reinterpret_cast<int4*>(smem + LY::QUEUE_OFF) + warp * (NS + 1);  // pieces brought, for the consumer
+  Queued* queue = reinterpret_cast<Queued*>(smem + LY::QUEUE_OFF) + warp * LY::NQ;
   uint64_t* win = reinterpret_cast<uint64_t*>(smem + LY::WIN_OFF) + warp * 32;
-  int win_base = 0, brought = 0;
-  const int bs_shift = __ffs(bs) - 1;
+  Walk* walk = reinterpret_cast<Walk*>(smem + LY::WALK_OFF) + warp;
+  const ulonglong2* win_at = nullptr;  // the next tile's two chunks
+  int win_left = 0;                    // tiles the window still holds
 
-  auto look_up = [&]() {  // the next 32 chunks of the walk's segment: where their codes start
-    win_base = 2 * wt;
-    const int tok = (win_base + lane) * 16;
-    uint64_t off = 0;
-    if (tok < wL) {
-      int phys = __ldg(p.block_tables + (size_t)wb * p.max_blocks_per_seq + (tok >> bs_shift));
+  auto file_piece = [&](Walk& w) {
+    const int nt = tiles_of(w.L);
+    w.end = min(nt, w.t + w.left);
+    w.left -= w.end - w.t;
+    if (lane == 0) {
+      Queued& q = queue[w.filed % LY::NQ];
+      *reinterpret_cast<int4*>(&q) = make_int4(w.b, w.g, w.L, w.t);
+      q.seg_start = w.seg_start;
+    }
+    ++w.filed;
+    w.seg_start += nt;  // empty sequences take no room on the line: the next segment follows at once
+  };
+  auto look_up = [&](Walk& w) {  // where the codes of the next 32 chunks of the piece are
+    const int tok = (2 * w.t + lane) * 16;
+    uint64_t off = ~0ull;        // no such chunk
+    if (tok < w.L) {
+      const int bs = p.block_size;
+      int phys = __ldg(p.block_tables + (size_t)w.b * p.max_blocks_per_seq + (tok >> (__ffs(bs) - 1)));
       if (phys < 0 || phys >= p.num_blocks) {  // broken caller invariant: record, read block 0 instead
         PA_RECORD_ERROR(PA_ERRBIT_INDEX);
         phys = 0;
       }
-      off = (uint64_t)(uint32_t)phys * code_block + (uint32_t)(wg * bs + (tok & (bs - 1))) * LY::ROWB;
+      const uint32_t code_block = p.num_kv_heads * bs * LY::ROWB;  // bytes; below 2^31 (checked on the host)
+      off = (uint64_t)(uint32_t)phys * code_block + (uint32_t)(w.g * bs + (tok & (bs - 1))) * LY::ROWB;
     }
+    win_left = min(16, w.end - w.t);
+    w.t += win_left;
     __syncwarp();
     win[lane] = off;
+    if (lane == 0) *walk = w;
+    win_at = reinterpret_cast<const ulonglong2*>(win);
     __syncwarp();
   };
-  auto open_piece = [&]() {
-    wend = min(tiles_of(wL), wt + left);
-    left -= wend - wt;
-    if (lane == 0) queue[brought % (NS + 1)] = make_int4(wb, wg, wL, wt);
-    ++brought;
-    look_up();
+  auto next_window = [&]() {
+    Walk w = *walk;
+    if (w.t == w.end) {  // the next segment; sequences without tokens have no tiles
+      w.t = 0;
+      if (++w.g == p.num_kv_heads) {
+        w.g = 0;
+        do w.L = len_of(++w.b);
+        while (w.L == 0 && w.b < p.batch - 1);
+      }
+      file_piece(w);
+    }
+    look_up(w);
   };
-  auto bring = [&](uint32_t stage) {  // the walk's next tile into the stage at this shared address
-    if (2 * wt == win_base + 32) look_up();
-    const ulonglong2 off = *reinterpret_cast<const ulonglong2*>(win + (2 * wt - win_base));
-    const bool two = wL - wt * kTile > 16;
+  auto bring = [&](uint32_t stage, bool more) {  // the walk's next tile into the stage at this shared address
+    const ulonglong2 off = *win_at++;
+    const uint8_t* k0 = kbase + off.x;
+    const uint8_t* v0 = k0 + p.v_codes;
 #pragma unroll
     for (int e = 0; e < PER; ++e) {
-      cp_async16(stage + LY::K_OFF + code_dst[e], kbase + off.x + 512 * e);
-      cp_async16(stage + LY::V_OFF + code_dst[e], vbase + off.x + 512 * e);
+      cp_async16(stage + LY::K_OFF + code_dst[e], k0 + 512 * e);
+      cp_async16(stage + LY::V_OFF + code_dst[e], v0 + 512 * e);
     }
+    const bool two = (uint32_t)(off.y >> 32) != 0xffffffffu;
     if (two) {
+      const uint8_t* k1 = kbase + off.y;
+      const uint8_t* v1 = k1 + p.v_codes;
 #pragma unroll
       for (int e = 0; e < PER; ++e) {
-        cp_async16(stage + LY::K_OFF + 16 * LY::ROWB + code_dst[e], kbase + off.y + 512 * e);
-        cp_async16(stage + LY::V_OFF + 16 * LY::ROWB + code_dst[e], vbase + off.y + 512 * e);
+        cp_async16(stage + LY::K_OFF + 16 * LY::ROWB + code_dst[e], k1 + 512 * e);
+        cp_async16(stage + LY::V_OFF + 16 * LY::ROWB + code_dst[e], v1 + 512 * e);
       }
     }
     if (par_run < 4 && (two || !(par_run & 1)))
       cp_async16(stage + par_dst, par_base + (((par_run & 1) ? off.y : off.x) >> 3));
-    if (++wt == wend && left > 0) {  // the next segment; sequences without tokens have no tiles
-      wt = 0;
-      if (++wg == Hkv) {
-        wg = 0;
-        do wL = len_of(++wb);
-        while (wL == 0 && wb < B - 1);
-      }
-      open_piece();
-    }
+    if (--win_left == 0 && more) next_window();
   };
-  if (tiles > 0) open_piece();
+  if (tiles > 0) {
+    w0.left = tiles;
+    file_piece(w0);
+    look_up(w0);
+  }
 
   // The cache, q and the output may be in use by the preceding kernel (programmatic dependent launch; lengths and
   // block tables are not its outputs): wait for it before the first load of them and before any write.
   asm volatile("griddepcontrol.wait;" ::: "memory");
 #pragma unroll
   for (int s = 0; s < NS; ++s) {
-    if (s < tiles) bring(ring + s * LY::STAGE);
+    if (s < tiles) bring(ring + s * LY::STAGE, s + 1 < tiles);
     cp_async_commit();
   }
   // sequences without a token: zeros, and a log-sum-exp of -inf
@@ -683,25 +761,37 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
 
   // ---- pieces and their tiles
   S st;
-  int stage_at = 0;  // byte offset of the current stage
-  for (int k = 0, piece = 0; k < tiles; ++piece) {
-    const int4 d = queue[piece % (NS + 1)];  // written before a warp barrier that this warp has passed
-    const int b = d.x, kvh = d.y, L = d.z, t0 = d.w, nt = tiles_of(L), t1 = min(nt, t0 + tiles - k);
-    // q is on its way while the tile lands
-    st.begin(reinterpret_cast<const uint8_t*>(p.q) + ((size_t)b * p.num_q_heads + (size_t)kvh * G) * D * 2, p.scale_log2,
-             lane);
-    for (int t = t0; t < t1; ++t, ++k) {
-      cp_async_wait<NS - 1>();
-      __syncwarp();
-      st.template tile<LY>(smem + LY::RING_OFF + warp * LY::RING + stage_at, L - t * kTile, lane);
-      __syncwarp();
-      if (k + NS < tiles) bring(ring + stage_at);
-      cp_async_commit();
-      stage_at = stage_at == (NS - 1) * LY::STAGE ? 0 : stage_at + LY::STAGE;
+  int stage_at = 0, to_bring = tiles - NS;  // byte offset of the current stage; tiles still to be brought in
+  for (int todo = tiles, piece = 0; todo > 0; ++piece) {
+    const Queued& d = queue[piece % LY::NQ];  // written before a warp barrier that this warp has passed
+    int rem;  // tokens of the segment from the current tile on
+    {
+      const int4 e = *reinterpret_cast<const int4*>(&d);
+      rem = e.z - e.w * kTile;
+      int m = min((rem + kTile - 1) / kTile, todo);   // the piece's tiles
+      todo -= m;
+      // q is on its way while the tile lands
+      st.begin(reinterpret_cast<const uint8_t*>(p.q) + ((size_t)e.x * p.num_q_heads + (size_t)e.y * G) * D * 2,
+               p.scale_log2, lane);
+      do {
+        cp_async_wait<NS - 1>();
+        __syncwarp();
+        st.template tile<LY>(smem + LY::RING_OFF + warp * LY::RING + stage_at, smem + LY::CONV_OFF + warp * LY::CONV, rem,
+                             lane);
+        __syncwarp();
+        if (to_bring > 0) bring(ring + stage_at, to_bring > 1);
+        --to_bring;
+        cp_async_commit();
+        stage_at = stage_at == (NS - 1) * LY::STAGE ? 0 : stage_at + LY::STAGE;
+        rem -= kTile;
+      } while (--m);
     }
     st.finish();
+    const int4 de = *reinterpret_cast<const int4*>(&d);
+    const int b = de.x, kvh = de.y;
+    const bool head = de.w == 0, tail = rem <= 0;
     const int g = lane >> 2, c = lane & 3;
-    if (t0 == 0 && t1 == nt) {
+    if (head && tail) {
       T* out = reinterpret_cast<T*>(p.out) + ((size_t)b * p.num_q_heads + (size_t)kvh * G) * D;
 #pragma unroll
       for (int n = 0; n < S::NT; ++n)
@@ -725,7 +815,7 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
             p.lse[(size_t)b * p.num_q_heads + (size_t)kvh * G + h] = (st.R[n][e] + __log2f(st.l[n][e])) * kLn2;
         }
     } else {
-      const int which = k == tiles;  // the warp's last piece lies in its ring, which is done with
+      const int which = todo == 0;  // the warp's last piece lies in its ring, which is done with
       float* part = reinterpret_cast<float*>(which ? smem + LY::RING_OFF + warp * LY::RING
                                                    : smem + LY::PART_OFF + warp * LY::PART);
 #pragma unroll
@@ -751,13 +841,12 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
         Piece pc;
         pc.b = b;
         pc.g = kvh;
-        pc.flags = F_VALID | (t0 == 0 ? F_HEAD : 0) | (t1 == nt ? F_TAIL : 0);
-        pc.nt = nt;
-        pc.seg_start = seg_start;
+        pc.flags = F_VALID | (head ? F_HEAD : 0) | (tail ? F_TAIL : 0);
+        pc.nt = tiles_of(de.z);
+        pc.seg_start = d.seg_start;
         pieces[2 * warp + which] = pc;
       }
     }
-    seg_start += nt;  // empty sequences take no room on the line: the next segment follows at once
   }
   // let the next programmatically launched kernel begin its set-up; it waits for this grid before it touches memory
   asm volatile("griddepcontrol.launch_dependents;");
@@ -1046,10 +1135,10 @@ extern "C" int pa_decode_int4(const void* q, const void* k_codes, const void* v_
   p.q = q;
   p.out = out;
   p.lse = lse_out;
-  p.base[0] = (const uint8_t*)k_codes;
-  p.base[1] = (const uint8_t*)v_codes;
-  p.base[2] = (const uint8_t*)k_params;
-  p.base[3] = (const uint8_t*)v_params;
+  p.k_codes = (const uint8_t*)k_codes;
+  p.k_params = (const uint8_t*)k_params;
+  p.v_codes = (long long)((intptr_t)v_codes - (intptr_t)k_codes);
+  p.v_params = (long long)((intptr_t)v_params - (intptr_t)k_params);
   p.block_tables = block_tables;
   p.context_lens = context_lens;
   p.ws_cnt = reinterpret_cast<int*>(ws);
