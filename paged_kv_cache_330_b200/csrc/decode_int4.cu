@@ -15,7 +15,7 @@
 // What a warp holds of a segment is a piece: a whole segment is written out at once, a partial one goes to
 // shared memory, and after the one barrier at the end of the tiles the pieces of a segment are joined, first
 // within the CTA, then, for the at most two segments that a CTA shares with its neighbours, through the
-// workspace by the warp that counts last (a counter per head, no waiting).  The joining order is the order of
+// workspace by the CTA that counts last (a counter per segment, no waiting).  The joining order is the order of
 // the line, so results do not depend on timing.
 //
 // Mathematics.  Products run on mma.m16n8k16 (fp16 in, fp32 out) with tokens (scores) or columns (PV) as the 16
@@ -51,6 +51,7 @@ using namespace pa;
 constexpr int kTile = 32;            // tokens per tile: two 16-token chunks, each within one block
 constexpr int kLens = 512;            // sequences whose lengths a CTA keeps in shared memory
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kGroup = 8;            // CTAs whose shares of a segment are joined first, where a segment has many
 constexpr float kGuess = -8.f;       // a piece's first reference: fits when its largest weight * V scale is 2^-5 .. 2^7
 constexpr float kUnit = 16777216.f;  // 2^24: what a code's fp16 subnormal stands for, inverted
 
@@ -64,7 +65,8 @@ struct Params {
   long long v_params;
   const int32_t* block_tables;
   const int32_t* context_lens;
-  int* ws_cnt;   // [batch * Hq] CTAs that have added their share of a head (zero between calls)
+  int* ws_cnt;   // [batch * Hkv] CTAs that have added their share of a segment (zero between calls)
+  int* ws_grp;   // [slots] the same within a group of CTAs (zero between calls)
   float* ws_r;   // [slots][G] reference R of a share
   float* ws_l;   // [slots][G]
   float* ws_o;   // [slots][G][D]
@@ -189,6 +191,16 @@ __device__ __forceinline__ void cp_async_wait() {
 // Floor division of a >= 0 by b > 0; `narrow` (uniform) says both fit in 32 bits: the 64-bit one is a long sequence.
 __device__ __forceinline__ long long udiv(long long a, long long b, bool narrow) {
   return narrow ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// One more at a counter that starts at zero, with device scope: what the block wrote before (its barrier passed) is
+// visible to whoever counts last, and the last finds everybody's.  The last one (of n) leaves the counter at zero.
+__device__ __forceinline__ bool count_last(int* cnt, int n) {
+  int old;
+  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(old) : "l"(cnt) : "memory");
+  if (old != n - 1) return false;
+  *cnt = 0;
+  return true;
 }
 
 constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;  // a nibble of each half, worth 2^-24 and 2^-20
@@ -587,6 +599,13 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
   const int B = p.batch, Hkv = p.num_kv_heads, bs = p.block_size;
   const int cap = p.max_blocks_per_seq * bs;
   if (lane == 0) pieces[2 * warp].flags = pieces[2 * warp + 1].flags = 0;
+  // The block tables come from HBM on their first use: ask for them (a line a thread, at most) while the lengths are
+  // added up.
+  {
+    const size_t line = (size_t)cta * (NW * 32) + threadIdx.x, bytes = (size_t)B * p.max_blocks_per_seq * 4;
+    if (line * 128 < bytes)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const uint8_t*>(p.block_tables) + line * 128));
+  }
 
   // ---- the line: thread i counts the tiles of sequences [i * per, (i + 1) * per), a scan within every warp; each warp
   // then looks its first tile up in the scans
@@ -903,7 +922,7 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
   const bool cut1 = runs > 1 && lacks_tail;
   const int shared = (cut0 + cut1) * G;  // (segment, head) items of cut segments: the warps take them in turn
   // 1. this CTA's shares of them, to the workspace: slot segment + CTA (a CTA holds at most one share of a segment,
-  // and neighbouring segments share at most one CTA); then one fence, and all counts at once
+  // and neighbouring segments share at most one CTA)
   for (int item = warp; item < shared; item += NW) {
     const int first = item < G && cut0 ? first0 : first1, h = item % G;
     float M, den, acc[DPL];
@@ -917,27 +936,32 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
       p.ws_l[row] = den;
     }
   }
-  int done = 0;          // lane i: the warp's item i is complete
-  int c0 = 0, n_sh = 0;  // its first CTA and its number of shares
-  if (warp < shared) {
-    const int item = warp + NW * lane;
-    const int first = item < G && cut0 ? first0 : first1;
-    const int b = __shfl_sync(0xffffffffu, pc.b, first), kvh = __shfl_sync(0xffffffffu, pc.g, first);
-    const int nt = __shfl_sync(0xffffffffu, pc.nt, first);
-    const long long s0 = __shfl_sync(0xffffffffu, pc.seg_start, first);
-    __threadfence();  // the shares are visible device-wide before they are counted
-    __syncwarp();
-    if (item < shared) {
-      c0 = (int)udiv((s0 + 1) * ctas - 1, total, narrow);
-      n_sh = (int)udiv((s0 + nt) * ctas - 1, total, narrow) - c0 + 1;
-      int* cnt = p.ws_cnt + (size_t)b * p.num_q_heads + (size_t)kvh * G + item % G;
-      done = atomicAdd(cnt, 1) == n_sh - 1;
-      if (done) *cnt = 0;  // nobody else counts here any more: the next call finds zero
-    }
+  // The cut segments (0: of the first run, 1: of the last): lane 0 or 1 of every warp, then all lanes of it.
+  size_t seg = 0;
+  int c0 = 0, n_sh = 0;  // the CTAs that hold shares
+  if (lane < 2 && (lane == 0 ? cut0 : cut1)) {
+    const Piece& mine = pieces[lane == 0 ? first0 : first1];
+    seg = (size_t)mine.b * Hkv + mine.g;
+    c0 = (int)udiv((mine.seg_start + 1) * ctas - 1, total, narrow);
+    n_sh = (int)udiv((mine.seg_start + mine.nt) * ctas - 1, total, narrow) - c0 + 1;
   }
-  // 2. segments that lie within the CTA
+  // A segment with many shares is joined by groups of kGroup CTAs first: one SM reads shares at little more than
+  // 100 GB/s.
+  const int gf = max(c0, cta / kGroup * kGroup);
+  const bool grouped = n_sh > 2 * kGroup;
+  int* cnt = grouped ? p.ws_grp + seg + gf : p.ws_cnt + seg;
+  int n = grouped ? min(c0 + n_sh, (cta / kGroup + 1) * kGroup) - gf : n_sh;  // shares to join now, from slot0 on
+  size_t slot0 = seg + (grouped ? gf : c0), slots = slot0;
+  int step = 1;
+  bool again = grouped;
+  int* done_s = reinterpret_cast<int*>(smem + LY::SCAN_OFF);
+  if (shared) {
+    __syncthreads();  // the CTA's shares are written
+    if (warp == 0 && lane < 2) done_s[lane] = n > 0 && count_last(cnt, n);
+  }
+  // 2. meanwhile the segments that lie within the CTA
   const int whole = (runs - cut0 - cut1) * G;
-  for (int item = (warp + NW - shared % NW) % NW; item < whole; item += NW) {
+  for (int item = NW - 1 - warp; item < whole; item += NW) {
     const int first = run_first(item / G + cut0), h = item % G;
     float M, den, acc[DPL];
     join(first, h, M, den, acc);
@@ -950,86 +974,100 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
       reinterpret_cast<uint32_t*>(out)[j] = Elt<DT>::from_f2(acc[2 * j] * inv, acc[2 * j + 1] * inv);
     if (p.lse && lane == 0) p.lse[at] = (M + __log2f(den)) * kLn2;
   }
-  // 3. the shares of cut segments that this warp counted last, joined: SG shares at a time, 4 columns a lane, U loads
-  // in flight
-  unsigned todo = __ballot_sync(0xffffffffu, done);
-  if (todo) __threadfence();
-  constexpr int LPS = D / 4, SG = 32 / LPS, U = 16 / SG;
-  for (; todo; todo &= todo - 1) {
-    const int j = __ffs(todo) - 1, item = warp + NW * j, h = item % G;
-    const int first = item < G && cut0 ? first0 : first1;
-    const int n = __shfl_sync(0xffffffffu, n_sh, j), from = __shfl_sync(0xffffffffu, c0, j);
-    const int b = __shfl_sync(0xffffffffu, pc.b, first), kvh = __shfl_sync(0xffffffffu, pc.g, first);
-    const size_t row0 = ((size_t)b * Hkv + kvh + from) * G + h;
-    const float* rp = p.ws_r + row0;
-    const float* lp = p.ws_l + row0;
-    const int sg = lane / LPS;
-    const float* op = p.ws_o + row0 * D + (lane % LPS) * 4;
-    float4 v[U];  // the first shares' values, asked for before the weights are known
+  if (!shared) return;
+  // 3. cut segments whose shares this CTA counted last: a thread takes 4 columns of a head, 8 shares at a time
+  constexpr int QUADS = G * D / 4, PASSES = (QUADS + NW * 32 - 1) / (NW * 32), U = 8;
+  for (int which = 0; which < 2; ++which) {
+    for (bool first_level = true;; first_level = false) {
+      __syncthreads();
+      if (!done_s[which]) break;
+      const int n_ = __shfl_sync(0xffffffffu, n, which), step_ = __shfl_sync(0xffffffffu, step, which);
+      const size_t slot0_ = __shfl_sync(0xffffffffu, slot0, which), slots_ = __shfl_sync(0xffffffffu, slots, which);
+      const size_t seg_ = __shfl_sync(0xffffffffu, seg, which);
+      const bool again_ = __shfl_sync(0xffffffffu, again, which);
+      float4 acc[PASSES];
+      float M[PASSES], den[PASSES];
 #pragma unroll
-    for (int u = 0; u < U; ++u) v[u] = __ldcg(reinterpret_cast<const float4*>(op + (size_t)min(u * SG + sg, n - 1) * G * D));
-    float r0 = 0.f, l0 = 0.f, M = -INFINITY;
-    for (int i = lane; i < n; i += 32) {
-      const float li = __ldcg(lp + (size_t)i * G), ri = __ldcg(rp + (size_t)i * G);
-      if (i == lane) r0 = ri, l0 = li;
-      M = fmaxf(M, li > 0.f ? ri + __log2f(li) : -INFINITY);
-    }
-    M = warp_max(M);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float den = 0.f;
-    for (int base = 0; base < n; base += 32) {
-      const int i = base + lane;
-      float w = 0.f;
-      if (i < n) {
-        const float li = base ? __ldcg(lp + (size_t)i * G) : l0, ri = base ? __ldcg(rp + (size_t)i * G) : r0;
-        w = li > 0.f ? exp2f(ri - M) : 0.f;
-        den = fmaf(w, li, den);
-      }
-      const int cnt = min(32, n - base);
-      for (int i0 = 0; i0 < cnt; i0 += SG * U) {
-        if (base + i0 > 0)
+      for (int ps = 0; ps < PASSES; ++ps) {
+        acc[ps] = make_float4(0.f, 0.f, 0.f, 0.f);
+        M[ps] = -INFINITY;
+        den[ps] = 0.f;
+        const int quad = ps * NW * 32 + threadIdx.x, h = quad / (D / 4), col = quad % (D / 4) * 4;
+        if (quad >= QUADS) break;
+        for (int i0 = 0; i0 < n_; i0 += U) {
+          float r[U], l[U];
+          float4 v[U];
 #pragma unroll
-          for (int u = 0; u < U; ++u)
-            v[u] = __ldcg(reinterpret_cast<const float4*>(op + (size_t)min(base + i0 + u * SG + sg, n - 1) * G * D));
+          for (int u = 0; u < U; ++u) {
+            const int i = min(i0 + u, n_ - 1);  // share i is in slot0 for i = 0, in slots + i * step for the others
+            const size_t row = (i == 0 ? slot0_ : slots_ + (size_t)i * step_) * G + h;
+            r[u] = __ldcg(p.ws_r + row);
+            l[u] = i0 + u < n_ ? __ldcg(p.ws_l + row) : 0.f;
+            v[u] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + row * D + col));
+          }
+          float top = M[ps];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int at = i0 + u * SG + sg;
-          const float wi = __shfl_sync(0xffffffffu, w, at & 31);
-          if (at < cnt) {
-            acc.x = fmaf(wi, v[u].x, acc.x); acc.y = fmaf(wi, v[u].y, acc.y);
-            acc.z = fmaf(wi, v[u].z, acc.z); acc.w = fmaf(wi, v[u].w, acc.w);
+          for (int u = 0; u < U; ++u) top = fmaxf(top, l[u] > 0.f ? r[u] + __log2f(l[u]) : -INFINITY);
+          const float f = M[ps] > -INFINITY ? exp2f(M[ps] - top) : 0.f;
+          M[ps] = top;
+          den[ps] *= f;
+          acc[ps].x *= f; acc[ps].y *= f; acc[ps].z *= f; acc[ps].w *= f;
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const float w = l[u] > 0.f ? exp2f(r[u] - top) : 0.f;
+            den[ps] = fmaf(w, l[u], den[ps]);
+            acc[ps].x = fmaf(w, v[u].x, acc[ps].x); acc[ps].y = fmaf(w, v[u].y, acc[ps].y);
+            acc[ps].z = fmaf(w, v[u].z, acc[ps].z); acc[ps].w = fmaf(w, v[u].w, acc[ps].w);
           }
         }
       }
-    }
-    den = warp_sum(den);
+      const bool partial = first_level && again_;
+      if (partial) __syncthreads();  // the group's shares are read: their joint share takes the first one's slot
 #pragma unroll
-    for (int o = LPS; o < 32; o <<= 1) {
-      acc.x += __shfl_xor_sync(0xffffffffu, acc.x, o); acc.y += __shfl_xor_sync(0xffffffffu, acc.y, o);
-      acc.z += __shfl_xor_sync(0xffffffffu, acc.z, o); acc.w += __shfl_xor_sync(0xffffffffu, acc.w, o);
+      for (int ps = 0; ps < PASSES; ++ps) {
+        const int quad = ps * NW * 32 + threadIdx.x, h = quad / (D / 4), col = quad % (D / 4) * 4;
+        if (quad >= QUADS) break;
+        if (partial) {
+          const size_t row = slot0_ * G + h;
+          *reinterpret_cast<float4*>(p.ws_o + row * D + col) = acc[ps];
+          if (col == 0) {
+            p.ws_r[row] = M[ps];
+            p.ws_l[row] = den[ps];
+          }
+        } else {
+          const size_t at = seg_ * G + h;  // batch * Hq + head
+          const float inv = 1.f / den[ps];
+          uint2 u;
+          u.x = Elt<DT>::from_f2(acc[ps].x * inv, acc[ps].y * inv);
+          u.y = Elt<DT>::from_f2(acc[ps].z * inv, acc[ps].w * inv);
+          *reinterpret_cast<uint2*>(reinterpret_cast<T*>(p.out) + at * D + col) = u;
+          if (p.lse && col == 0) p.lse[at] = (M[ps] + __log2f(den[ps])) * kLn2;
+        }
+      }
+      if (!partial) break;
+      // count the groups; the last one joins their joint shares
+      slot0 = seg + c0;
+      slots = seg + c0 / kGroup * kGroup;
+      step = kGroup;
+      n = (c0 + n_sh - 1) / kGroup - c0 / kGroup + 1;
+      __syncthreads();
+      if (warp == 0 && lane == which) done_s[lane] = count_last(p.ws_cnt + seg, n);
     }
-    const size_t at = (size_t)b * p.num_q_heads + (size_t)kvh * G + h;
-    if (sg == 0) {
-      const float inv = 1.f / den;
-      uint2 u;
-      u.x = Elt<DT>::from_f2(acc.x * inv, acc.y * inv);
-      u.y = Elt<DT>::from_f2(acc.z * inv, acc.w * inv);
-      *reinterpret_cast<uint2*>(reinterpret_cast<T*>(p.out) + at * D + lane * 4) = u;
-    }
-    if (p.lse && lane == 0) p.lse[at] = (M + __log2f(den)) * kLn2;
   }
 }
 
 // ------------------------------------------------------------------ host side
+constexpr int kWarps = 12;  // consumer warps of a CTA (G 16: 8)
+
 template <int D, int G>
 struct Shape {
-  static constexpr int NW = G == 16 ? 8 : 16;
+  static constexpr int NW = G == 16 ? 8 : kWarps;
   static constexpr int NS = 2;
 };
 
 struct Plan {
   int grid;
-  size_t off_r, off_l, off_o, bytes;
+  size_t off_grp, off_r, off_l, off_o, bytes;
 };
 
 bool make_plan(int batch, int Hq, int Hkv, int D, int max_context_len, int num_partitions, Plan* pl) {
@@ -1037,12 +1075,22 @@ bool make_plan(int batch, int Hq, int Hkv, int D, int max_context_len, int num_p
   if (!valid_head_dim(D) || !valid_group(Hq / Hkv)) return false;
   if ((int64_t)batch * Hq >= (1ll << 31)) return false;
   const int G = Hq / Hkv;
-  // one CTA fills an SM; no more CTAs than leave each at least four tiles (were all contexts as long as they may be)
-  const int64_t tiles = (int64_t)batch * Hkv * ((max_context_len + (int64_t)kTile - 1) / kTile);
-  pl->grid = num_partitions ? num_partitions : (int)std::max<int64_t>(1, std::min<int64_t>(sm_count(), (tiles + 3) / 4));
+  // One CTA fills an SM.  A small batch takes no more CTAs than give every warp about two tiles (were all contexts as
+  // long as they may be), and a multiple of its segments, so that equal lengths are cut where CTAs meet or not at
+  // all: joining across CTAs costs about 4 us.  (One sequence of 300 tokens, 8 KV heads: 8 CTAs 7 us, 20 CTAs 8.8 us.)
+  const int64_t segs = std::max<int64_t>(1, (int64_t)batch * Hkv);
+  const int64_t tiles = segs * ((max_context_len + (int64_t)kTile - 1) / kTile);
+  const int64_t sms = sm_count(), want = (tiles + 2 * kWarps - 1) / (2 * kWarps);
+  int64_t grid = std::min(sms, std::max<int64_t>(1, want));
+  if (segs <= sms) {
+    const int64_t up = std::min(sms / segs, (grid + segs - 1) / segs) * segs;
+    if (up >= grid || up * 20 >= grid * 19) grid = up;
+  }
+  pl->grid = num_partitions ? num_partitions : (int)grid;
   auto align256 = [](size_t x) { return (x + 255) & ~size_t(255); };
   const size_t slots = (size_t)batch * Hkv + pl->grid;
-  pl->off_r = align256((size_t)batch * Hq * 4);
+  pl->off_grp = align256((size_t)batch * Hkv * 4);
+  pl->off_r = pl->off_grp + align256(slots * 4);
   pl->off_l = pl->off_r + align256(slots * G * 4);
   pl->off_o = pl->off_l + align256(slots * G * 4);
   pl->bytes = pl->off_o + align256(slots * G * D * 4);
@@ -1142,6 +1190,7 @@ extern "C" int pa_decode_int4(const void* q, const void* k_codes, const void* v_
   p.block_tables = block_tables;
   p.context_lens = context_lens;
   p.ws_cnt = reinterpret_cast<int*>(ws);
+  p.ws_grp = reinterpret_cast<int*>(ws + pl.off_grp);
   p.ws_r = reinterpret_cast<float*>(ws + pl.off_r);
   p.ws_l = reinterpret_cast<float*>(ws + pl.off_l);
   p.ws_o = reinterpret_cast<float*>(ws + pl.off_o);
