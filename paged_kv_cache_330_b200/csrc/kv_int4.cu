@@ -128,11 +128,10 @@ __global__ void __launch_bounds__(256) write_kv_int4_kernel(const WriteArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int TPR = D / 16, NG = D / 64;
   const int rows = a.hq + 2 * a.hkv;
-  for (int64_t base = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) & ~31ll; base < a.total;
-       base += (int64_t)gridDim.x * blockDim.x) {
-    const int i = (int)base + (threadIdx.x & 31);
+  {
+    const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
     const bool in = i < a.total;
-    const int row = in ? i / TPR : 0, j = i % TPR;
+    const int row = in ? (int)i / TPR : 0, j = (int)i % TPR;
     const int t = row / rows, r = row - t * rows;
     const bool isq = ROPE && r < a.hq, isv = r >= a.hq + a.hkv;
     const int h = isq ? r : (isv ? r - a.hq - a.hkv : r - a.hq);
@@ -198,7 +197,7 @@ __global__ void __launch_bounds__(256) write_kv_int4_kernel(const WriteArgs a) {
         hi2 = fmaxf(hi2, __shfl_xor_sync(0xffffffffu, hi2, o));
       }
     }
-    if (!live || isq) continue;
+    if (!live || isq) return;
     float s1, z1, inv1, s2, z2, inv2;
     const uint32_t p1 = group_params<DT>(lo1, hi1, s1, z1, inv1);
     uint32_t p2 = p1;
@@ -225,49 +224,39 @@ __global__ void __launch_bounds__(256) write_kv_int4_kernel(const WriteArgs a) {
   }
 }
 
-// Block copy: CTA (pair, part); a part is up to 1024 16-byte vectors of the pair's four runs.  Every thread
-// has its four loads in flight before the first store.
-constexpr int kCopyPart = 1024;
+// Block copy: CTA (pair, part); a part is up to kCopyLoads * 256 16-byte vectors of the pair's four runs, end to end.
+// Every thread has its loads in flight before the first store.
+constexpr int kCopyLoads = 5;
 __global__ void __launch_bounds__(256) copy_blocks_int4_kernel(const int32_t* __restrict__ pairs, int code_vecs,
-                                                               int param_vecs, int num_blocks, uint4* kc, uint4* vc,
-                                                               uint4* kp, uint4* vp) {
+                                                               int param_vecs, int num_blocks, int per_part, uint4* kc,
+                                                               uint4* vc, uint4* kp, uint4* vp) {
   const int32_t src = __ldg(pairs + 2 * (int64_t)blockIdx.x), dst = __ldg(pairs + 2 * (int64_t)blockIdx.x + 1);
   if (src < 0 || src >= num_blocks || dst < 0 || dst >= num_blocks) {
     if (threadIdx.x == 0 && blockIdx.y == 0) PA_RECORD_ERROR(PA_ERRBIT_INDEX);
     return;
   }
   const int total = 2 * (code_vecs + param_vecs);
-  for (int part = blockIdx.y * kCopyPart; part < total; part += gridDim.y * kCopyPart) {
-    uint4 u[kCopyPart / 256];
-    uint4* to[kCopyPart / 256];
+  for (int64_t part = blockIdx.y * (int64_t)per_part; part < total; part += (int64_t)gridDim.y * per_part) {
+    const int end = (int)min((int64_t)total, part + per_part);
+    uint4 u[kCopyLoads];
+    uint4* to[kCopyLoads];
 #pragma unroll
-    for (int e = 0; e < kCopyPart / 256; ++e) {
-      const int i = part + e * 256 + threadIdx.x;
+    for (int e = 0; e < kCopyLoads; ++e) {
+      const int i = (int)part + e * 256 + threadIdx.x;
       to[e] = nullptr;
-      if (i < total) {
-        uint4* base;
-        int64_t per = code_vecs;
-        int o = i;
-        if (i < code_vecs) {
-          base = kc;
-        } else if (i < 2 * code_vecs) {
-          base = vc;
-          o = i - code_vecs;
-        } else {
-          per = param_vecs;
-          o = i - 2 * code_vecs;
-          base = kp;
-          if (o >= param_vecs) {
-            base = vp;
-            o -= param_vecs;
-          }
-        }
-        u[e] = ld_plain_v4(base + src * per + o);
-        to[e] = base + dst * per + o;
+      if (i < end) {
+        const bool codes = i < 2 * code_vecs;
+        const int per = codes ? code_vecs : param_vecs;
+        int o = codes ? i : i - 2 * code_vecs;
+        const bool isv = o >= per;
+        if (isv) o -= per;
+        uint4* base = codes ? (isv ? vc : kc) : (isv ? vp : kp);
+        u[e] = ld_plain_v4(base + (int64_t)src * per + o);
+        to[e] = base + (int64_t)dst * per + o;
       }
     }
 #pragma unroll
-    for (int e = 0; e < kCopyPart / 256; ++e)
+    for (int e = 0; e < kCopyLoads; ++e)
       if (to[e]) st_v4(to[e], u[e]);
   }
 }
@@ -282,7 +271,9 @@ __device__ __forceinline__ uint4 expand8(uint32_t w, uint32_t param) {
   return pack8<DT>(x);
 }
 
-// Expansion: CTA (pair and K or V, part of the block's rows); rows in the order of the 16-bit block.
+// Expansion: CTA (pair and K or V, part of the block's rows); rows in the order of the 16-bit block; a thread has the
+// loads of kLoadItems items in flight before it expands the first.
+constexpr int kLoadItems = 4;
 template <int DT, int D>
 __global__ void __launch_bounds__(256) load_blocks_int4_kernel(const int32_t* __restrict__ pairs, int hkv,
                                                                int block_size, int num_blocks, int num_dst,
@@ -304,23 +295,33 @@ __global__ void __launch_bounds__(256) load_blocks_int4_kernel(const int32_t* __
   const uint32_t* params = (isv ? vp : kp) + src * rows * NG;
   uint4* out = (isv ? v : k) + dst * rows * (D / 8);
   const int total = (int)rows * TPR;
-  for (int i = blockIdx.y * blockDim.x + threadIdx.x; i < total; i += gridDim.y * blockDim.x) {
-    const int row = i / TPR, j = i % TPR;     // row = token * hkv + head of the 16-bit block
-    const int tok = row / hkv, h = row - tok * hkv;
-    const int64_t crow = (int64_t)h * block_size + tok;
-    uint32_t w1, w2, p1, p2;
-    if constexpr (NG == 2) {
-      const uint2 w = __ldg(reinterpret_cast<const uint2*>(codes + crow * (D / 8)) + j);
-      const uint2 p = __ldg(reinterpret_cast<const uint2*>(params + crow * NG));
-      w1 = w.x; w2 = w.y; p1 = p.x; p2 = p.y;
-    } else {
-      w1 = __ldg(codes + crow * (D / 8) + j);
-      w2 = __ldg(codes + crow * (D / 8) + j + 4);
-      p1 = p2 = __ldg(params + crow);
+  for (int64_t part = blockIdx.y * (int64_t)(kLoadItems * 256); part < total; part += (int64_t)gridDim.y * (kLoadItems * 256)) {
+    uint32_t w1[kLoadItems], w2[kLoadItems], p1[kLoadItems], p2[kLoadItems];
+#pragma unroll
+    for (int e = 0; e < kLoadItems; ++e) {
+      const int i = (int)part + e * 256 + threadIdx.x;
+      const int row = i / TPR, j = i % TPR;  // row = token * hkv + head of the 16-bit block
+      const int tok = row / hkv, h = row - tok * hkv;
+      const int64_t crow = (int64_t)h * block_size + tok;
+      if (i >= total) continue;
+      if constexpr (NG == 2) {
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(codes + crow * (D / 8)) + j);
+        const uint2 p = __ldg(reinterpret_cast<const uint2*>(params + crow * NG));
+        w1[e] = w.x; w2[e] = w.y; p1[e] = p.x; p2[e] = p.y;
+      } else {
+        w1[e] = __ldg(codes + crow * (D / 8) + j);
+        w2[e] = __ldg(codes + crow * (D / 8) + j + 4);
+        p1[e] = p2[e] = __ldg(params + crow);
+      }
     }
-    uint4* o = out + (int64_t)row * (D / 8) + j;
-    st_v4(o, expand8<DT>(w1, p1));
-    st_v4(o + TPR, expand8<DT>(w2, p2));
+#pragma unroll
+    for (int e = 0; e < kLoadItems; ++e) {
+      const int i = (int)part + e * 256 + threadIdx.x;
+      if (i >= total) continue;
+      uint4* o = out + (int64_t)(i / TPR) * (D / 8) + i % TPR;
+      st_v4(o, expand8<DT>(w1[e], p1[e]));
+      st_v4(o + TPR, expand8<DT>(w2[e], p2[e]));
+    }
   }
 }
 
@@ -337,9 +338,8 @@ bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0
 
 template <bool ROPE>
 int launch_write(const WriteArgs& a, int head_dim, int dtype, cudaStream_t st) {
-  int64_t blocks = ((int64_t)a.total + 255) / 256;
-  const int64_t cap = (int64_t)sm_count() * 8;  // at most one resident wave: every CTA strides over the items
-  if (blocks > cap) blocks = cap;
+  // one item a thread: the hardware keeps the SMs filled with fresh loads
+  const int64_t blocks = ((int64_t)a.total + 255) / 256;
   auto kern = dtype == PA_BF16
                   ? (head_dim == 128 ? write_kv_int4_kernel<PA_BF16, 128, ROPE> : write_kv_int4_kernel<PA_BF16, 64, ROPE>)
                   : (head_dim == 128 ? write_kv_int4_kernel<PA_F16, 128, ROPE> : write_kv_int4_kernel<PA_F16, 64, ROPE>);
@@ -432,10 +432,11 @@ extern "C" int pa_copy_blocks_int4(const int32_t* pairs, int num_pairs, void* k_
   if (reinterpret_cast<uintptr_t>(pairs) & 3u) return PA_ERR_ALIGN;
   const int rows = num_kv_heads * block_size;
   const int code_vecs = rows * (head_dim / 32), param_vecs = rows * (head_dim / 64) / 4;
-  const int parts = (2 * (code_vecs + param_vecs) + kCopyPart - 1) / kCopyPart;
+  const int total = 2 * (code_vecs + param_vecs), parts = (total + kCopyLoads * 256 - 1) / (kCopyLoads * 256);
+  const int per_part = (total + parts - 1) / parts;  // equal parts
   const dim3 grid((unsigned)num_pairs, (unsigned)(parts > 65535 ? 65535 : parts));
   copy_blocks_int4_kernel<<<grid, 256, 0, (cudaStream_t)stream>>>(pairs, code_vecs, param_vecs, num_blocks,
-                                                                  (uint4*)k_codes, (uint4*)v_codes, (uint4*)k_params,
+                                                                  per_part, (uint4*)k_codes, (uint4*)v_codes, (uint4*)k_params,
                                                                   (uint4*)v_params);
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
@@ -453,7 +454,7 @@ extern "C" int pa_load_blocks_int4(const int32_t* pairs, int num_pairs, const vo
   if (!pairs || num_pairs >= (1 << 30)) return PA_ERR_INVALID;
   if (reinterpret_cast<uintptr_t>(pairs) & 3u) return PA_ERR_ALIGN;
   const int64_t total = (int64_t)num_kv_heads * block_size * (head_dim / 16);
-  const int64_t parts = (total + 1023) / 1024;  // four items a thread
+  const int64_t parts = (total + kLoadItems * 256 - 1) / (kLoadItems * 256);
   auto kern = dtype == PA_BF16 ? (head_dim == 128 ? load_blocks_int4_kernel<PA_BF16, 128> : load_blocks_int4_kernel<PA_BF16, 64>)
                                : (head_dim == 128 ? load_blocks_int4_kernel<PA_F16, 128> : load_blocks_int4_kernel<PA_F16, 64>);
   const dim3 grid((unsigned)num_pairs * 2u, (unsigned)(parts > 65535 ? 65535 : parts));
