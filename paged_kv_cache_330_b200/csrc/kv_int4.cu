@@ -61,32 +61,18 @@ __device__ __forceinline__ uint4 pack8(const float* x) {
                     Elt<DT>::from_f2(x[6], x[7]));
 }
 
-// Scale, zero point (as the 16-bit word pair s | z << 16) and reciprocal of a group with extremes lo, hi.
-template <int DT>
-__device__ __forceinline__ uint32_t group_params(float lo, float hi, float& s, float& z, float& inv) {
-  s = Elt<DT>::to_f2(Elt<DT>::from_f2(__fsub_rn(__fdiv_rn(hi, 15.f), __fdiv_rn(lo, 15.f)), 0.f)).x;
-  if (s >= 1.17549435e-38f) {
-    z = __fdiv_rn(lo, s);
-    inv = __fdiv_rn(1.f, s);
-  } else {
-    s = fabsf(lo);
-    z = lo > 0.f ? 1.f : (lo < 0.f ? -1.f : 0.f);
-    inv = 0.f;  // with the shift below every code is 0
-  }
-  const uint32_t w = Elt<DT>::from_f2(s, z);
-  z = Elt<DT>::to_f2(w).y;
-  return w;
-}
-
-// 8 values -> a word of 8 codes; x becomes the values that the codes stand for (unrounded).
+// 8 values -> a word of 8 codes; x becomes the values that the codes stand for (unrounded).  Clamping before rounding
+// gives what rounding first gives (the ends are whole), and keeps the sum with 1.5 * 2^23 exact but for its one
+// rounding, to a whole number, half to even; the code is then in that sum's low bits.
 __device__ __forceinline__ uint32_t encode8(float* x, float s, float z, float inv) {
+  constexpr float kWhole = 12582912.f;
   uint32_t word = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    int c = __float2int_rn(__fsub_rn(__fmul_rn(x[i], inv), z));
-    c = inv == 0.f ? 0 : min(15, max(0, c));
-    word |= (uint32_t)c << (4 * i);
-    x[i] = __fmul_rn(s, __fadd_rn((float)c, z));
+    const float t = fminf(fmaxf(__fsub_rn(__fmul_rn(x[i], inv), z), 0.f), 15.f);
+    const float m = __fadd_rn(inv == 0.f ? 0.f : t, kWhole);
+    word += (__float_as_uint(m) - __float_as_uint(kWhole)) << (4 * i);
+    x[i] = __fmul_rn(s, __fadd_rn(__fsub_rn(m, kWhole), z));
   }
   return word;
 }
@@ -137,6 +123,14 @@ __global__ void __launch_bounds__(256) write_kv_int4_kernel(const WriteArgs a) {
     const int h = isq ? r : (isv ? r - a.hq - a.hkv : r - a.hq);
     bool live = in;
     int64_t pos = 0, slot = 0;
+    // the row's values are on their way while its position and slot are looked up
+    float x1[8], x2[8];
+    uint4 u1 = make_uint4(0, 0, 0, 0), u2 = u1;
+    if (in) {
+      const uint4* src = (isq ? a.q : (isv ? a.v : a.k)) + (isq ? (int64_t)t * a.hq + h : (int64_t)t * a.hkv + h) * (D / 8) + j;
+      u1 = ld_plain_v4(src);
+      u2 = ld_plain_v4(src + TPR);
+    }
     if (ROPE && in) {
       pos = __ldg(a.positions + t);
       if (pos < 0 || pos >= a.max_position) {  // broken caller invariant: record once per token, write nothing
@@ -151,10 +145,7 @@ __global__ void __launch_bounds__(256) write_kv_int4_kernel(const WriteArgs a) {
     }
     const int64_t src_row = isq ? (int64_t)t * a.hq + h : (int64_t)t * a.hkv + h;
     const int64_t vec = src_row * (D / 8) + j;
-    float x1[8], x2[8];
     if (live) {
-      const uint4* src = (isq ? a.q : (isv ? a.v : a.k)) + vec;
-      uint4 u1 = ld_plain_v4(src), u2 = ld_plain_v4(src + TPR);
       unpack8<DT>(u1, x1);
       unpack8<DT>(u2, x2);
       if (ROPE && !isv) {
@@ -183,6 +174,7 @@ __global__ void __launch_bounds__(256) write_kv_int4_kernel(const WriteArgs a) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) x1[e] = x2[e] = 0.f;
     }
+    if (ROPE && __all_sync(0xffffffffu, isq || !in)) return;
     float lo1 = min8(x1), hi1 = max8(x1), lo2 = min8(x2), hi2 = max8(x2);
     if constexpr (NG == 1) {
       lo1 = fminf(lo1, lo2);
@@ -197,12 +189,29 @@ __global__ void __launch_bounds__(256) write_kv_int4_kernel(const WriteArgs a) {
         hi2 = fmaxf(hi2, __shfl_xor_sync(0xffffffffu, hi2, o));
       }
     }
+    // Four quotients a group, each an IEEE division: taken by one lane each (two a lane, not eight) and handed round.
+    // Lane j of the row: group (j / 2) mod n, the even lane hi / 15 and lo / s, the odd one lo / 15 and 1 / s.
+    const bool odd = j & 1, second = NG == 2 && (j & 2);
+    const float lo = second ? lo2 : lo1, hi = second ? hi2 : hi1;
+    const float q15 = __fdiv_rn(odd ? lo : hi, 15.f), other = __shfl_xor_sync(0xffffffffu, q15, 1);
+    float s = Elt<DT>::to_f2(Elt<DT>::from_f2(odd ? __fsub_rn(other, q15) : __fsub_rn(q15, other), 0.f)).x;
+    const bool alike = !(s >= 1.17549435e-38f);
+    float quot = __fdiv_rn(odd ? 1.f : lo, alike ? 1.f : s);
+    if (alike) {
+      s = fabsf(lo);
+      quot = odd ? 0.f : (lo > 0.f ? 1.f : (lo < 0.f ? -1.f : 0.f));  // 1 / s taken as 0: every code is 0
+    }
+    const uint32_t pword = Elt<DT>::from_f2(s, quot);  // (s, z) in the even lane
+    if (!odd) quot = Elt<DT>::to_f2(pword).y;
+    const float s1 = __shfl_sync(0xffffffffu, s, 0, TPR), z1 = __shfl_sync(0xffffffffu, quot, 0, TPR),
+                inv1 = __shfl_sync(0xffffffffu, quot, 1, TPR);
+    float s2 = s1, z2 = z1, inv2 = inv1;
+    if constexpr (NG == 2) {
+      s2 = __shfl_sync(0xffffffffu, s, 2, TPR);
+      z2 = __shfl_sync(0xffffffffu, quot, 2, TPR);
+      inv2 = __shfl_sync(0xffffffffu, quot, 3, TPR);
+    }
     if (!live || isq) return;
-    float s1, z1, inv1, s2, z2, inv2;
-    const uint32_t p1 = group_params<DT>(lo1, hi1, s1, z1, inv1);
-    uint32_t p2 = p1;
-    s2 = s1; z2 = z1; inv2 = inv1;
-    if constexpr (NG == 2) p2 = group_params<DT>(lo2, hi2, s2, z2, inv2);
     const uint32_t w1 = encode8(x1, s1, z1, inv1), w2 = encode8(x2, s2, z2, inv2);
     const int64_t blk = slot / a.block_size;
     const int64_t crow = (blk * a.hkv + h) * a.block_size + (slot - blk * a.block_size);
@@ -210,12 +219,11 @@ __global__ void __launch_bounds__(256) write_kv_int4_kernel(const WriteArgs a) {
     uint32_t* pw = (isv ? a.vp : a.kp) + crow * NG;
     if constexpr (NG == 2) {
       reinterpret_cast<uint2*>(cw)[j] = make_uint2(w1, w2);
-      if (j == 0) *reinterpret_cast<uint2*>(pw) = make_uint2(p1, p2);
     } else {
       cw[j] = w1;
       cw[j + 4] = w2;
-      if (j == 0) *pw = p1;
     }
+    if (!odd && j < 2 * NG) pw[j >> 1] = pword;
     uint4* held = isv ? a.v_out : a.k_out;
     if (held) {
       st_v4(held + vec, pack8<DT>(x1));
