@@ -560,9 +560,35 @@ def decode_int8(q, k_codes, v_codes, k_scales, v_scales, block_tables, context_l
 
 
 # ---------------------------------------------------------------------------------------------- INT4 cache
-# These calls are short on the device (a few microseconds for one decode step's write), so the host's share is kept
-# small: one combined check of everything, the detailed checkers only to word an error, plain integers to ctypes, and
-# the current stream's handle without a stream object.
+# These calls are short on the device (2 to 6 us for one decode step's rows), so their arguments are checked and
+# marshalled by the native module _calls (binding/calls.cpp) instead of attribute by attribute here.  It calls the C
+# entry, or says that an argument is not as it has to be; the checkers below then word what is wrong.
+_NATIVE = None
+_NATIVE_ENTRIES = ("pa_write_kv_int4", "pa_rope_write_kv_int4", "pa_copy_blocks_int4", "pa_load_blocks_int4",
+                   "pa_decode_int4")
+_WRONG, _NEEDS_WORKSPACE = 1, 2
+
+
+def _native():
+    global _NATIVE
+    if _NATIVE is None:
+        import importlib
+        _torch()  # the module links against torch's libraries
+        m = importlib.import_module("._calls", __name__)
+        m.bind(*(ctypes.cast(getattr(lib, f), _vp).value for f in _NATIVE_ENTRIES))
+        _NATIVE = m
+    return _NATIVE
+
+
+def _handle(stream, lead):
+    """The C handle of a given stream; the stream has to belong to lead's device."""
+    if stream is None:
+        return None
+    if stream.device_index != lead.get_device():
+        _device_slow(stream, (lead,))
+    return stream.cuda_stream
+
+
 def _int4_caches(k_codes, v_codes, k_params, v_params):
     """Codes uint8 [NB, Hkv, bs, D/2] (both alike), parameters [NB, Hkv, bs, D/64, 2] (both alike, bf16 or fp16):
     words what is wrong with them, if anything is; returns (NB, bs, Hkv, D)."""
@@ -579,58 +605,22 @@ def _int4_caches(k_codes, v_codes, k_params, v_params):
     return cs[0], cs[2], cs[1], cs[3] * 2
 
 
-def _int4_ok(k_codes, v_codes, k_params, v_params, dt, dev):
-    """Whether the four cache tensors are as _int4_caches wants them, parameters in dtype dt, all on device dev."""
-    cs, u8 = k_codes.shape, _torch().uint8
-    return (len(cs) == 4 and v_codes.shape == cs and k_params.shape == (cs[0], cs[1], cs[2], cs[3] // 32, 2)
-            and v_params.shape == k_params.shape and cs[3] % 32 == 0 and k_codes.dtype is u8 and v_codes.dtype is u8
-            and k_params.dtype is dt and v_params.dtype is dt and k_codes.get_device() == dev
-            and v_codes.get_device() == dev and k_params.get_device() == dev and v_params.get_device() == dev
-            and k_codes.is_contiguous() and v_codes.is_contiguous() and k_params.is_contiguous()
-            and v_params.is_contiguous())
-
-
-def _like(t, dt, shape, dev):
-    """A tensor argument (None: not given) of this dtype, shape and device, contiguous."""
-    return t is None or (t.dtype is dt and t.shape == shape and t.get_device() == dev and t.is_contiguous())
-
-
-def _here(stream, dev):
-    """dev is the current CUDA device, and a given stream's."""
-    return dev >= 0 and dev == _torch()._C._cuda_getDevice() and (stream is None or stream.device_index == dev)
-
-
-def _stream_int(stream, dev):
-    return stream.cuda_stream if stream is not None else _torch()._C._cuda_getCurrentRawStream(dev)
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
 def write_kv_int4(k, v, slot_mapping, k_codes, v_codes, k_params, v_params, k_out=None, v_out=None,
                   stream=None) -> None:
     """Quantise k, v [T, Hkv, D] (the parameters' dtype) into the INT4 cache rows of slot_mapping int64 [T]
     (-1 = skip).  k_out, v_out (like k, v; they may be k, v): the rows as the cache now holds them."""
-    torch = _torch()
-    ks, dt, dev = k.shape, k.dtype, k.get_device()
-    if not (len(ks) == 3 and (dt is torch.bfloat16 or dt is torch.float16)
-            and _int4_ok(k_codes, v_codes, k_params, v_params, dt, dev) and k_codes.shape[1] == ks[1]
-            and k_codes.shape[3] * 2 == ks[2] and k.is_contiguous() and _like(v, dt, ks, dev)
-            and _like(slot_mapping, torch.int64, ks[:1], dev) and _like(k_out, dt, ks, dev)
-            and _like(v_out, dt, ks, dev) and _here(stream, dev)):
+    st = _native().write_kv_int4(k, v, slot_mapping, k_codes, v_codes, k_params, v_params, k_out, v_out,
+                                _handle(stream, k))
+    if st == _WRONG:
+        torch = _torch()
         _, _, Hkv, D = _int4_caches(k_codes, v_codes, k_params, v_params)
         _contig(k, v, slot_mapping, k_out, v_out)
-        T = int(ks[0]) if len(ks) > 0 else -1
+        T = int(k.shape[0]) if k.dim() > 0 else -1
         for name, x in (("k", k), ("v", v), ("k_out", k_out), ("v_out", v_out)):
             if x is not None:
                 _want(name, x, dtype=k_params.dtype, shape=(T, Hkv, D))
         _want("slot_mapping", slot_mapping, dtype=torch.int64, shape=(T,))
         _device_slow(stream, (k, v, slot_mapping, k_codes, v_codes, k_params, v_params, k_out, v_out))
-    NB, Hkv, bs, _ = k_codes.shape
-    st = lib.pa_write_kv_int4(k.data_ptr(), v.data_ptr(), slot_mapping.data_ptr(), ks[0], k_codes.data_ptr(),
-                              v_codes.data_ptr(), k_params.data_ptr(), v_params.data_ptr(), _addr(k_out), _addr(v_out),
-                              NB, bs, Hkv, ks[2], dt is torch.bfloat16, _stream_int(stream, dev))
     if st:
         _check(st, "pa_write_kv_int4")
 
@@ -640,41 +630,28 @@ def rope_write_kv_int4(q, k, v, positions, cos_table, sin_table, slot_mapping, k
     """rope_write_kv into the INT4 cache: q and k turned by their positions' table rows, k and v quantised into
     their slots.  Returns q_out (a new tensor unless given; q_out=q rotates in place).  k_out, v_out as in
     write_kv_int4."""
-    torch = _torch()
-    qs, ks, dt, dev, cts = q.shape, k.shape, q.dtype, q.get_device(), cos_table.shape
-    if not (len(qs) == 3 and len(ks) == 3 and len(cts) == 2 and (dt is torch.bfloat16 or dt is torch.float16)
-            and _int4_ok(k_codes, v_codes, k_params, v_params, dt, dev) and k_codes.shape[1] == ks[1]
-            and k_codes.shape[3] * 2 == qs[2] == ks[2] and qs[0] == ks[0] and cts[1] * 2 == qs[2]
-            and q.is_contiguous() and _like(k, dt, ks, dev) and _like(v, dt, ks, dev)
-            and _like(positions, torch.int64, ks[:1], dev) and _like(slot_mapping, torch.int64, ks[:1], dev)
-            and _like(cos_table, torch.float32, cts, dev) and _like(sin_table, torch.float32, cts, dev)
-            and _like(q_out, dt, qs, dev) and _like(k_out, dt, ks, dev) and _like(v_out, dt, ks, dev)
-            and _here(stream, dev)):
+    if q_out is None:
+        q_out = _torch().empty_like(q)
+    st = _native().rope_write_kv_int4(q, k, v, positions, cos_table, sin_table, slot_mapping, k_codes, v_codes, k_params,
+                                     v_params, q_out, k_out, v_out, _handle(stream, q))
+    if st == _WRONG:
+        torch = _torch()
         _, _, Hkv, D = _int4_caches(k_codes, v_codes, k_params, v_params)
         _contig(q, q_out, k, v, positions, cos_table, sin_table, slot_mapping, k_out, v_out)
         _want("q", q, dtype=k_params.dtype, ndim=3)
-        T, Hq = int(qs[0]), int(qs[1])
+        T, Hq = int(q.shape[0]), int(q.shape[1])
         _want("q", q, shape=(T, Hq, D))
-        if q_out is not None:
-            _want("q_out", q_out, dtype=dt, shape=(T, Hq, D))
+        _want("q_out", q_out, dtype=q.dtype, shape=(T, Hq, D))
         for name, x in (("k", k), ("v", v), ("k_out", k_out), ("v_out", v_out)):
             if x is not None:
-                _want(name, x, dtype=dt, shape=(T, Hkv, D))
+                _want(name, x, dtype=q.dtype, shape=(T, Hkv, D))
         _want("positions", positions, dtype=torch.int64, shape=(T,))
         _want("slot_mapping", slot_mapping, dtype=torch.int64, shape=(T,))
         _want("cos_table", cos_table, dtype=torch.float32, ndim=2)
-        _want("cos_table", cos_table, shape=(cts[0], D // 2))
-        _want("sin_table", sin_table, dtype=torch.float32, shape=cts)
+        _want("cos_table", cos_table, shape=(cos_table.shape[0], D // 2))
+        _want("sin_table", sin_table, dtype=torch.float32, shape=cos_table.shape)
         _device_slow(stream, (q, q_out, k, v, positions, cos_table, sin_table, slot_mapping, k_codes, v_codes, k_params,
                               v_params, k_out, v_out))
-    if q_out is None:
-        q_out = torch.empty_like(q)
-    NB, Hkv, bs, _ = k_codes.shape
-    st = lib.pa_rope_write_kv_int4(q.data_ptr(), q_out.data_ptr(), k.data_ptr(), v.data_ptr(), positions.data_ptr(),
-                                   cos_table.data_ptr(), sin_table.data_ptr(), cts[0], slot_mapping.data_ptr(), qs[0],
-                                   qs[1], k_codes.data_ptr(), v_codes.data_ptr(), k_params.data_ptr(),
-                                   v_params.data_ptr(), _addr(k_out), _addr(v_out), NB, bs, Hkv, qs[2],
-                                   dt is torch.bfloat16, _stream_int(stream, dev))
     if st:
         _check(st, "pa_rope_write_kv_int4")
     return q_out
@@ -683,19 +660,13 @@ def rope_write_kv_int4(q, k, v, positions, cos_table, sin_table, slot_mapping, k
 def copy_blocks_int4(pairs, k_codes, v_codes, k_params, v_params, stream=None) -> None:
     """pairs int32 [n, 2] (src, dst) on the device: copy whole blocks of the INT4 codes and parameters.  A source
     may repeat; destinations are distinct from one another and from every source."""
-    torch = _torch()
-    ps, dt, dev = pairs.shape, k_params.dtype, pairs.get_device()
-    if not (len(ps) == 2 and ps[1] == 2 and (dt is torch.bfloat16 or dt is torch.float16)
-            and _like(pairs, torch.int32, ps, dev) and _int4_ok(k_codes, v_codes, k_params, v_params, dt, dev)
-            and _here(stream, dev)):
+    st = _native().copy_blocks_int4(pairs, k_codes, v_codes, k_params, v_params, _handle(stream, pairs))
+    if st == _WRONG:
         _int4_caches(k_codes, v_codes, k_params, v_params)
         _contig(pairs)
-        _want("pairs", pairs, dtype=torch.int32, ndim=2)
-        _want("pairs", pairs, shape=(ps[0], 2))
+        _want("pairs", pairs, dtype=_torch().int32, ndim=2)
+        _want("pairs", pairs, shape=(pairs.shape[0], 2))
         _device_slow(stream, (pairs, k_codes, v_codes, k_params, v_params))
-    NB, Hkv, bs, B2 = k_codes.shape
-    st = lib.pa_copy_blocks_int4(pairs.data_ptr(), ps[0], k_codes.data_ptr(), v_codes.data_ptr(), k_params.data_ptr(),
-                                 v_params.data_ptr(), NB, bs, Hkv, B2 * 2, _stream_int(stream, dev))
     if st:
         _check(st, "pa_copy_blocks_int4")
 
@@ -704,23 +675,17 @@ def load_blocks_int4(pairs, k_codes, v_codes, k_params, v_params, k_cache, v_cac
     """pairs int32 [n, 2] (src, dst) on the device: expand block src of the INT4 cache into block dst of the
     16-bit cache k_cache, v_cache [NB2, bs, Hkv, D] (the parameters' dtype), where prefill_chunk and
     decode_cascade read."""
-    torch = _torch()
-    ps, xs, dt, dev = pairs.shape, k_cache.shape, k_cache.dtype, pairs.get_device()
-    if not (len(ps) == 2 and ps[1] == 2 and len(xs) == 4 and (dt is torch.bfloat16 or dt is torch.float16)
-            and _like(pairs, torch.int32, ps, dev) and _int4_ok(k_codes, v_codes, k_params, v_params, dt, dev)
-            and xs[1:] == (k_codes.shape[2], k_codes.shape[1], k_codes.shape[3] * 2) and _like(k_cache, dt, xs, dev)
-            and _like(v_cache, dt, xs, dev) and _here(stream, dev)):
+    st = _native().load_blocks_int4(pairs, k_codes, v_codes, k_params, v_params, k_cache, v_cache,
+                                   _handle(stream, pairs))
+    if st == _WRONG:
         _, bs, Hkv, D = _int4_caches(k_codes, v_codes, k_params, v_params)
         _contig(pairs, k_cache, v_cache)
         _want("k_cache", k_cache, dtype=k_params.dtype, ndim=4)
-        _want("k_cache", k_cache, shape=(xs[0], bs, Hkv, D))
-        _want("v_cache", v_cache, dtype=k_params.dtype, shape=xs)
-        _want("pairs", pairs, dtype=torch.int32, ndim=2)
-        _want("pairs", pairs, shape=(ps[0], 2))
+        _want("k_cache", k_cache, shape=(k_cache.shape[0], bs, Hkv, D))
+        _want("v_cache", v_cache, dtype=k_params.dtype, shape=k_cache.shape)
+        _want("pairs", pairs, dtype=_torch().int32, ndim=2)
+        _want("pairs", pairs, shape=(pairs.shape[0], 2))
         _device_slow(stream, (pairs, k_codes, v_codes, k_params, v_params, k_cache, v_cache))
-    st = lib.pa_load_blocks_int4(pairs.data_ptr(), ps[0], k_codes.data_ptr(), v_codes.data_ptr(), k_params.data_ptr(),
-                                 v_params.data_ptr(), k_codes.shape[0], k_cache.data_ptr(), v_cache.data_ptr(), xs[0],
-                                 xs[1], xs[2], xs[3], dt is torch.bfloat16, _stream_int(stream, dev))
     if st:
         _check(st, "pa_load_blocks_int4")
 
@@ -737,38 +702,35 @@ def decode_int4(q, k_codes, v_codes, k_params, v_params, block_tables, context_l
                 scale: float, out=None, lse=None, workspace=None, num_partitions: int = 0, stream=None):
     """Decode over the INT4 cache: q [B, Hq, D] in the parameters' dtype; returns out [B, Hq, D].  lse (float32
     [B, Hq], optional) receives the log-sum-exp of each (sequence, head)'s scores, as decode_lse gives it."""
-    torch = _torch()
-    qs, bts, dt, dev = q.shape, block_tables.shape, q.dtype, q.get_device()
-    if not (len(qs) == 3 and len(bts) == 2 and bts[0] == qs[0] and (dt is torch.bfloat16 or dt is torch.float16)
-            and _int4_ok(k_codes, v_codes, k_params, v_params, dt, dev) and k_codes.shape[3] * 2 == qs[2]
-            and q.is_contiguous() and _like(block_tables, torch.int32, bts, dev)
-            and _like(context_lens, torch.int32, qs[:1], dev) and _like(out, dt, qs, dev)
-            and _like(lse, torch.float32, qs[:2], dev) and _here(stream, dev)
-            and (workspace is None or (workspace.get_device() == dev and workspace.is_contiguous()))):
+    if out is None:
+        out = _torch().empty_like(q)
+    handle = _handle(stream, q)
+    call = _native().decode_int4
+    st = call(q, k_codes, v_codes, k_params, v_params, block_tables, context_lens, max_context_len, scale, out, lse,
+              workspace, num_partitions, handle)
+    if st == _NEEDS_WORKSPACE:  # zero-filled once; every call leaves it zeroed again (a given one the library checks)
+        need = decode_int4_plan(q.shape[0], q.shape[1], k_codes.shape[1], q.shape[2], max_context_len, num_partitions)[2]
+        workspace = _torch().zeros(need, dtype=_torch().uint8, device=q.device)
+        st = call(q, k_codes, v_codes, k_params, v_params, block_tables, context_lens, max_context_len, scale, out, lse,
+                  workspace, num_partitions, handle)
+    if st == _WRONG:
+        torch = _torch()
         _, _, _, D = _int4_caches(k_codes, v_codes, k_params, v_params)
         _contig(q, block_tables, context_lens, out, lse, workspace)
         _want("q", q, dtype=k_params.dtype, ndim=3)
-        B, Hq = int(qs[0]), int(qs[1])
+        B, Hq = int(q.shape[0]), int(q.shape[1])
         _want("q", q, shape=(B, Hq, D))
         _want("block_tables", block_tables, dtype=torch.int32, ndim=2)
-        _want("block_tables", block_tables, shape=(B, bts[1]))
+        _want("block_tables", block_tables, shape=(B, block_tables.shape[1]))
         _want("context_lens", context_lens, dtype=torch.int32, shape=(B,))
-        if out is not None:
-            _want("out", out, dtype=dt, shape=qs)
+        _want("out", out, dtype=q.dtype, shape=q.shape)
         if lse is not None:
             _want("lse", lse, dtype=torch.float32, shape=(B, Hq))
+        for name, x in (("max_context_len", max_context_len), ("num_partitions", num_partitions)):
+            if not -(1 << 31) <= int(x) < 1 << 31:
+                raise ValueError(f"{name} must fit in 32 bits, got {x}")
+        float(scale)
         _device_slow(stream, (q, k_codes, v_codes, k_params, v_params, block_tables, context_lens, out, lse, workspace))
-    NB, Hkv, bs, _ = k_codes.shape
-    B, Hq, D = qs
-    if out is None:
-        out = torch.empty_like(q)
-    if workspace is None:  # zero-filled once; every call leaves it zeroed again (a given one is checked by the library)
-        workspace = torch.zeros(decode_int4_plan(B, Hq, Hkv, D, max_context_len, num_partitions)[2], dtype=torch.uint8,
-                                device=q.device)
-    st = lib.pa_decode_int4(q.data_ptr(), k_codes.data_ptr(), v_codes.data_ptr(), k_params.data_ptr(),
-                            v_params.data_ptr(), block_tables.data_ptr(), bts[1], context_lens.data_ptr(), B, Hq, Hkv, D,
-                            bs, NB, max_context_len, scale, dt is torch.bfloat16, workspace.data_ptr(), workspace.nbytes,
-                            num_partitions, out.data_ptr(), _addr(lse), _stream_int(stream, dev))
     if st:
         _check(st, "pa_decode_int4")
     return out

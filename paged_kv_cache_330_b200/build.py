@@ -3,16 +3,20 @@
     python paged_kv_cache_330_b200/build.py [--debug-ptxas]
 
 Each source compiles to an object under ``_build/`` (in parallel), then nvcc
-links the shared library next to this file.  Nothing is JIT-compiled at
-import time: the binding loads the prebuilt library or fails.
+links the shared library next to this file.  ``binding/calls.cpp``, the native
+half of the Python binding, compiles to ``_calls.so`` against the installed
+torch's headers.  Nothing is JIT-compiled at import time: the binding loads the
+prebuilt libraries or fails.
 """
 
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +24,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libpaged_attn.so")
+CALLS = os.path.join(PKG, "_calls.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC = os.environ.get("NVCC", "nvcc")
@@ -46,12 +51,32 @@ def _compile(src: str, extra: list[str]) -> str:
     return obj
 
 
+def _build_calls() -> None:
+    """binding/calls.cpp -> _calls.so (host code only; torch is found without importing it)."""
+    src = os.path.join(PKG, "binding", "calls.cpp")
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    # the installed torch counts as a source: its headers fix the layout of a tensor
+    deps = [src, os.path.join(INCLUDE, "paged_attn.h"), os.path.join(torch, "version.py")]
+    if os.path.exists(CALLS) and all(os.path.getmtime(CALLS) >= os.path.getmtime(d) for d in deps):
+        return
+    cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(torch, "include"), "-isystem", os.path.join(torch, "include/torch/csrc/api/include"),
+           "-isystem", cuda, src, "-o", CALLS, "-L", os.path.join(torch, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
+
+
 def build(verbose: bool = False, ptxas_info: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     extra = ["-Xptxas", "-v"] if ptxas_info else []
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
+        calls = ex.submit(_build_calls)
         objs = list(ex.map(lambda s: _compile(s, extra if s.endswith(".cu") else []), srcs))
+        calls.result()
     newest = max(os.path.getmtime(o) for o in objs)
     if not os.path.exists(LIB) or os.path.getmtime(LIB) < newest:
         cmd = [NVCC, *ARCH, "-shared", "-o", LIB, *objs, "-cudart", "static"]

@@ -107,15 +107,15 @@ DEVICE_MSG = "device calls take CUDA tensors"
 
 
 @pytest.fixture
-def trapped(monkeypatch):
-    real = pa.lib
-
-    class Trap:
-        def __getattr__(self, name):
-            if "int4" in name:
-                raise AssertionError(f"{name} reached the library from a CPU-tensor call")
-            return getattr(real, name)
-    monkeypatch.setattr(pa, "lib", Trap())
+def trapped():
+    """The native half of the binding bound to entries that only note that they were reached."""
+    reached = []
+    note = ctypes.CFUNCTYPE(ctypes.c_int)(lambda: reached.append(1) or 0)
+    native = pa._native()
+    native.bind(*[ctypes.cast(note, ctypes.c_void_p).value] * 5)
+    yield
+    native.bind(*(ctypes.cast(getattr(pa.lib, f), ctypes.c_void_p).value for f in pa._NATIVE_ENTRIES))
+    assert not reached
 
 
 def _raises(msg, fn, *a, **kw):
@@ -217,6 +217,18 @@ def test_decode_int4_binding(trapped):
 
 
 def test_wrong_kinds_reach_no_library_call(trapped):
-    with pytest.raises((ctypes.ArgumentError, AttributeError, TypeError, ValueError)):
-        pa.decode_int4(np.zeros((1, 2, 128)), *_cache(), torch.zeros(1, 1, dtype=torch.int32),
-                       torch.ones(1, dtype=torch.int32), 16, 0.1)
+    """Arrays, numbers, None, sparse tensors and numbers out of range: a Python error, no call and no crash."""
+    q, bt, lens = _rows(T=1, H=2), torch.zeros(1, 1, dtype=torch.int32), torch.ones(1, dtype=torch.int32)
+    errors = (AttributeError, TypeError, ValueError, RuntimeError)
+    for x in (np.zeros((1, 2, 128)), 3, None, "q", q.to_sparse()):
+        with pytest.raises(errors):
+            pa.decode_int4(x, *_cache(), bt, lens, 16, 0.1)
+        with pytest.raises(errors):
+            pa.write_kv_int4(q, x, torch.zeros(1, dtype=torch.int64), *_cache())
+        with pytest.raises(errors):
+            pa.decode_int4(q, x, *_cache()[1:], bt, lens, 16, 0.1)
+    for bad in (dict(max_context_len=1 << 40), dict(max_context_len="16"), dict(scale="x"), dict(num_partitions=1.5)):
+        with pytest.raises(errors):
+            pa.decode_int4(q, *_cache(), bt, lens, **{"max_context_len": 16, "scale": 0.1, **bad})
+    for n in range(3):
+        assert pa._native().write_kv_int4(*[q] * n) == pa._WRONG
