@@ -98,6 +98,12 @@ struct Walk {
   long long pad2;
 };
 
+// Pieces of one segment within a CTA, for the joining step.
+struct Run {
+  unsigned mask;  // which pieces
+  int b, g, whole;
+};
+
 template <int D, int G, int NW, int NS>
 struct Layout {
   static constexpr int NG = D / 64, ROWB = D / 2, PARB = NG * 4;
@@ -116,8 +122,14 @@ struct Layout {
   static constexpr int SCAN_OFF = WIN_OFF + NW * 256;            // int64 [NW]: tiles of a warp's sequences
   static constexpr int INCL_OFF = WIN_OFF;                       // int64 [NW * 32]: the scan within the warps, at the start
   static constexpr int CONV_OFF = SCAN_OFF + NW * 8;             // CONV [NW]
+  static constexpr int JOIN_OFF = WIN_OFF;                       // Run [2 NW], weights and sums: after the tiles
+  static_assert(JOIN_OFF + 2 * NW * (16 + 12 * G) <= CONV_OFF + NW * CONV, "room for the joining step");
   static constexpr int LENS_OFF = CONV_OFF + NW * CONV;          // int [kLens]: lengths, for batches that fit
-  static constexpr int BYTES = LENS_OFF + kLens * 4;
+  // q rows of the pieces filed, for groups of heads small enough: their pieces may be short, and each would wait for q
+  static constexpr bool QS = G <= 4;
+  static constexpr int QB = QS ? G * D * 2 : 0;
+  static constexpr int QS_OFF = LENS_OFF + kLens * 4;            // QB [NW][NQ]
+  static constexpr int BYTES = QS_OFF + NW * NQ * QB;
   // Byte offset of word `word` (4 bytes) of row `row` among a tile's codes: 16-byte units of a row are exchanged so
   // that neighbouring rows' units lie in different banks.  Rows 8 apart are exchanged alike.
   static __device__ __forceinline__ int code_off(int row, int word) {
@@ -219,6 +231,7 @@ struct State {
   bool fresh;              // some head has met no non-zero V scale yet: its R is not set
 
   // qrows: the group's [G][D] rows of q.  A lane loads just the values its operands hold.
+  template <bool in_shared>
   __device__ __forceinline__ void begin(const uint8_t* qrows, float scale_log2, int lane) {
     const int g = lane >> 2, c = lane & 3;
     uint4 raw[NT][WPL];
@@ -231,7 +244,10 @@ struct State {
         // stored word WPL * c + i of a row: 8 values from `base` on
         const int base = D == 128 ? 64 * (i & 1) + 8 * (2 * c + (i >> 1)) : 8 * (2 * c + i);
         raw[nt][i] = make_uint4(0, 0, 0, 0);
-        if (nt * 8 + g < G) raw[nt][i] = __ldcg(reinterpret_cast<const uint4*>(qrows + ((nt * 8 + g) * D + base) * 2));
+        if (nt * 8 + g < G) {
+          const uint4* at = reinterpret_cast<const uint4*>(qrows + ((nt * 8 + g) * D + base) * 2);
+          raw[nt][i] = in_shared ? *at : __ldcg(at);
+        }
       }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -698,6 +714,16 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
     ++w.filed;
     w.seg_start += nt;  // empty sequences take no room on the line: the next segment follows at once
   };
+  auto q_rows = [&](int b, int kvh) {
+    return reinterpret_cast<const uint8_t*>(p.q) + ((size_t)b * p.num_q_heads + (size_t)kvh * G) * D * 2;
+  };
+  auto bring_q = [&](const Walk& w) {  // of the piece filed last, with its first tile
+    if constexpr (LY::QS) {
+      const uint8_t* src = q_rows(w.b, w.g);
+      const uint32_t dst = smem_u32(smem + LY::QS_OFF + (warp * LY::NQ + (w.filed - 1) % LY::NQ) * LY::QB);
+      for (int i = lane; i < LY::QB / 16; i += 32) cp_async16(dst + i * 16, src + i * 16);
+    }
+  };
   auto look_up = [&](Walk& w) {  // where the codes of the next 32 chunks of the piece are
     const int tok = (2 * w.t + lane) * 16;
     uint64_t off = ~0ull;        // no such chunk
@@ -729,6 +755,7 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
         while (w.L == 0 && w.b < p.batch - 1);
       }
       file_piece(w);
+      bring_q(w);
     }
     look_up(w);
   };
@@ -764,6 +791,7 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
   // The cache, q and the output may be in use by the preceding kernel (programmatic dependent launch; lengths and
   // block tables are not its outputs): wait for it before the first load of them and before any write.
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (tiles > 0) bring_q(w0);
 #pragma unroll
   for (int s = 0; s < NS; ++s) {
     if (s < tiles) bring(ring + s * LY::STAGE, s + 1 < tiles);
@@ -789,9 +817,13 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
       rem = e.z - e.w * kTile;
       int m = min((rem + kTile - 1) / kTile, todo);   // the piece's tiles
       todo -= m;
-      // q is on its way while the tile lands
-      st.begin(reinterpret_cast<const uint8_t*>(p.q) + ((size_t)e.x * p.num_q_heads + (size_t)e.y * G) * D * 2,
-               p.scale_log2, lane);
+      if constexpr (LY::QS) {
+        cp_async_wait<NS - 1>();
+        __syncwarp();
+        st.template begin<true>(smem + LY::QS_OFF + (warp * LY::NQ + piece % LY::NQ) * LY::QB, p.scale_log2, lane);
+      } else {  // q is on its way while the tile lands
+        st.template begin<false>(q_rows(e.x, e.y), p.scale_log2, lane);
+      }
       do {
         cp_async_wait<NS - 1>();
         __syncwarp();
@@ -871,7 +903,8 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
   asm volatile("griddepcontrol.launch_dependents;");
   __syncthreads();
 
-  // ---- join the pieces of each segment.  Lane i holds piece i of the CTA; a run is the pieces of one segment.
+  // ---- join the pieces of each segment.  Lane i holds piece i of the CTA; a run is the pieces of one segment.  (This
+  // code runs once a launch, so its instructions come from far: few of them, and threads side by side, count.)
   Piece pc;
   pc.flags = 0;
   pc.b = pc.g = pc.nt = 0;
@@ -880,67 +913,104 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
   const bool valid = pc.flags & F_VALID;
   const unsigned vmask = __ballot_sync(0xffffffffu, valid);
   if (vmask == 0) return;
+  Run* run_s = reinterpret_cast<Run*>(smem + LY::JOIN_OFF);
+  float* w_s = reinterpret_cast<float*>(run_s + 2 * NW);    // [2 NW][G]: weight of a piece within its run
+  float2* md_s = reinterpret_cast<float2*>(w_s + 2 * NW * G);  // [2 NW][G]: reference M and sum of a run
   const unsigned below = vmask & ((1u << lane) - 1u);
   const long long prev = __shfl_sync(0xffffffffu, pc.seg_start, below ? 31 - __clz(below) : lane);
-  const unsigned smask = __ballot_sync(0xffffffffu, valid && (!below || prev != pc.seg_start));
+  const bool starts = valid && (!below || prev != pc.seg_start);
+  const unsigned smask = __ballot_sync(0xffffffffu, starts);
   const int runs = __popc(smask);
-  auto run_first = [&](int r) {
-    const bool nth = (smask >> lane & 1) && __popc(smask & ((1u << lane) - 1u)) == r;
-    return __ffs(__ballot_sync(0xffffffffu, nth)) - 1;
-  };
+  const unsigned after = lane < 31 ? smask & ~((2u << lane) - 1u) : 0u;
+  const unsigned rmask = vmask & ~((1u << lane) - 1u) & (after ? (1u << (__ffs(after) - 1)) - 1u : 0xffffffffu);
+  const int end_flags = __shfl_sync(0xffffffffu, pc.flags, starts ? 31 - __clz(rmask) : lane);
+  const bool whole = (pc.flags & F_HEAD) && (end_flags & F_TAIL);
+  // Segments cut between CTAs: the first run or the last at most.
+  const bool cut0 = __shfl_sync(0xffffffffu, starts && !whole, __ffs(smask) - 1);
+  const bool cut1 = runs > 1 && __shfl_sync(0xffffffffu, starts && !whole, 31 - __clz(smask));
+  const int cuts = cut0 + cut1;
+  if (starts) {  // every warp writes the same table, and reads its own writes
+    Run r;
+    r.mask = rmask;
+    r.b = pc.b;
+    r.g = pc.g;
+    r.whole = whole;
+    run_s[__popc(smask & ((1u << lane) - 1u))] = r;
+  }
+  __syncwarp();
   auto part_of = [&](int i) {
     return reinterpret_cast<const float*>((i & 1) ? smem + LY::RING_OFF + (i >> 1) * LY::RING
                                                   : smem + LY::PART_OFF + (i >> 1) * LY::PART);
   };
-  constexpr int DPL = D / 32;
-  // The pieces of run `first` ... joined for head h: reference M (of the pieces' log-sum-exps, so nothing overflows),
-  // sum den and this lane's DPL columns, relative to M.
-  auto join = [&](int first, int h, float& M, float& den, float (&acc)[DPL]) {
-    const unsigned after = first < 31 ? smask & ~((2u << first) - 1u) : 0u;
-    const unsigned mask = vmask & ~((1u << first) - 1u) & (after ? (1u << (__ffs(after) - 1)) - 1u : 0xffffffffu);
-    const bool on = mask >> lane & 1;
-    const float* part = part_of(on ? lane : first);
-    const float R = on ? part[G * D + h] : -INFINITY, l = on ? part[G * D + G + h] : 0.f;
-    M = warp_max(l > 0.f ? R + __log2f(l) : -INFINITY);
-    const float w = l > 0.f ? exp2f(R - M) : 0.f;
-    den = warp_sum(w * l);
+  // weights: eight lanes to a (run, head)
+  for (int item = warp * 4 + (lane >> 3); item - (lane >> 3) < runs * G; item += NW * 4) {
+    const int r = min(item / G, runs - 1), h = item % G;
+    const unsigned mask = run_s[r].mask;
+    float R[(2 * NW + 7) / 8], l[(2 * NW + 7) / 8], M = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < DPL; ++j) acc[j] = 0.f;
-    for (unsigned m = mask; m; m &= m - 1) {
-      const int i = __ffs(m) - 1;
-      const float wi = __shfl_sync(0xffffffffu, w, i);
-      const float* o = part_of(i) + h * D + lane * DPL;
+    for (int k = 0; k < (2 * NW + 7) / 8; ++k) {
+      const int i = k * 8 + (lane & 7);
+      const bool on = mask >> i & 1;
+      R[k] = on ? part_of(i)[G * D + h] : 0.f;
+      l[k] = on ? part_of(i)[G * D + G + h] : 0.f;
+      M = fmaxf(M, l[k] > 0.f ? R[k] + __log2f(l[k]) : -INFINITY);  // of the pieces' log-sum-exps: nothing overflows
+    }
 #pragma unroll
-      for (int j = 0; j < DPL; ++j) acc[j] = fmaf(wi, o[j], acc[j]);
+    for (int o = 4; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float den = 0.f;
+#pragma unroll
+    for (int k = 0; k < (2 * NW + 7) / 8; ++k) {
+      const int i = k * 8 + (lane & 7);
+      const float w = l[k] > 0.f ? exp2f(R[k] - M) : 0.f;
+      den = fmaf(w, l[k], den);
+      if ((mask >> i & 1) && item < runs * G) w_s[i * G + h] = w;
+    }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+    if ((lane & 7) == 0 && item < runs * G) md_s[r * G + h] = make_float2(M, den);
+  }
+  __syncthreads();
+  // columns: a thread takes 4 of a head.  Cut segments first: this CTA's shares of them go to the workspace, slot
+  // segment + CTA (a CTA holds at most one share of a segment, and neighbouring segments share at most one CTA).
+  constexpr int QUADS = G * D / 4;
+  auto columns = [&](int from, int to) {
+    for (int q = from * QUADS + threadIdx.x; q < to * QUADS; q += NW * 32) {
+      const int k = q / QUADS, e = q - k * QUADS, h = e / (D / 4), col = e % (D / 4) * 4;
+      const int r = k >= cuts ? k - cuts + cut0 : (k == 0 && cut0 ? 0 : runs - 1);
+      const Run run = run_s[r];
+      const float2 md = md_s[r * G + h];
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (unsigned m = run.mask; m; m &= m - 1) {
+        const int i = __ffs(m) - 1;
+        const float w = w_s[i * G + h];
+        const float4 o = *reinterpret_cast<const float4*>(part_of(i) + h * D + col);
+        acc.x = fmaf(w, o.x, acc.x); acc.y = fmaf(w, o.y, acc.y);
+        acc.z = fmaf(w, o.z, acc.z); acc.w = fmaf(w, o.w, acc.w);
+      }
+      const size_t seg = (size_t)run.b * Hkv + run.g;
+      if (run.whole) {
+        const float inv = 1.f / md.y;
+        uint2 u;
+        u.x = Elt<DT>::from_f2(acc.x * inv, acc.y * inv);
+        u.y = Elt<DT>::from_f2(acc.z * inv, acc.w * inv);
+        *reinterpret_cast<uint2*>(reinterpret_cast<T*>(p.out) + (seg * G + h) * D + col) = u;
+        if (p.lse && col == 0) p.lse[seg * G + h] = (md.x + __log2f(md.y)) * kLn2;
+      } else {
+        const size_t row = (seg + cta) * G + h;
+        *reinterpret_cast<float4*>(p.ws_o + row * D + col) = acc;
+        if (col == 0) {
+          p.ws_r[row] = md.x;
+          p.ws_l[row] = md.y;
+        }
+      }
     }
   };
-  // Segments cut between CTAs: the first run if it lacks its segment's first tile or (being the last run, too) its last
-  // tile, and the last run if it lacks its last.
-  const int first0 = run_first(0), first1 = run_first(runs - 1), last = 31 - __clz(vmask);
-  const bool lacks_tail = !(__shfl_sync(0xffffffffu, pc.flags, last) & F_TAIL);
-  const bool cut0 = !(__shfl_sync(0xffffffffu, pc.flags, first0) & F_HEAD) || (runs == 1 && lacks_tail);
-  const bool cut1 = runs > 1 && lacks_tail;
-  const int shared = (cut0 + cut1) * G;  // (segment, head) items of cut segments: the warps take them in turn
-  // 1. this CTA's shares of them, to the workspace: slot segment + CTA (a CTA holds at most one share of a segment,
-  // and neighbouring segments share at most one CTA)
-  for (int item = warp; item < shared; item += NW) {
-    const int first = item < G && cut0 ? first0 : first1, h = item % G;
-    float M, den, acc[DPL];
-    join(first, h, M, den, acc);
-    const size_t seg = (size_t)__shfl_sync(0xffffffffu, pc.b, first) * Hkv + __shfl_sync(0xffffffffu, pc.g, first);
-    const size_t row = (seg + cta) * G + h;
-#pragma unroll
-    for (int j = 0; j < DPL; ++j) p.ws_o[row * D + lane * DPL + j] = acc[j];
-    if (lane == 0) {
-      p.ws_r[row] = M;
-      p.ws_l[row] = den;
-    }
-  }
+  columns(0, cuts);
   // The cut segments (0: of the first run, 1: of the last): lane 0 or 1 of every warp, then all lanes of it.
   size_t seg = 0;
   int c0 = 0, n_sh = 0;  // the CTAs that hold shares
   if (lane < 2 && (lane == 0 ? cut0 : cut1)) {
-    const Piece& mine = pieces[lane == 0 ? first0 : first1];
+    const Piece& mine = pieces[__ffs(run_s[lane == 0 ? 0 : runs - 1].mask) - 1];
     seg = (size_t)mine.b * Hkv + mine.g;
     c0 = (int)udiv((mine.seg_start + 1) * ctas - 1, total, narrow);
     n_sh = (int)udiv((mine.seg_start + mine.nt) * ctas - 1, total, narrow) - c0 + 1;
@@ -954,29 +1024,15 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
   size_t slot0 = seg + (grouped ? gf : c0), slots = slot0;
   int step = 1;
   bool again = grouped;
-  int* done_s = reinterpret_cast<int*>(smem + LY::SCAN_OFF);
-  if (shared) {
+  int* done_s = reinterpret_cast<int*>(smem + LY::LENS_OFF);
+  if (cuts) {
     __syncthreads();  // the CTA's shares are written
     if (warp == 0 && lane < 2) done_s[lane] = n > 0 && count_last(cnt, n);
   }
-  // 2. meanwhile the segments that lie within the CTA
-  const int whole = (runs - cut0 - cut1) * G;
-  for (int item = NW - 1 - warp; item < whole; item += NW) {
-    const int first = run_first(item / G + cut0), h = item % G;
-    float M, den, acc[DPL];
-    join(first, h, M, den, acc);
-    const size_t at = (size_t)__shfl_sync(0xffffffffu, pc.b, first) * p.num_q_heads +
-                      (size_t)__shfl_sync(0xffffffffu, pc.g, first) * G + h;
-    const float inv = 1.f / den;
-    T* out = reinterpret_cast<T*>(p.out) + at * D + lane * DPL;
-#pragma unroll
-    for (int j = 0; j < DPL / 2; ++j)
-      reinterpret_cast<uint32_t*>(out)[j] = Elt<DT>::from_f2(acc[2 * j] * inv, acc[2 * j + 1] * inv);
-    if (p.lse && lane == 0) p.lse[at] = (M + __log2f(den)) * kLn2;
-  }
-  if (!shared) return;
-  // 3. cut segments whose shares this CTA counted last: a thread takes 4 columns of a head, 8 shares at a time
-  constexpr int QUADS = G * D / 4, PASSES = (QUADS + NW * 32 - 1) / (NW * 32), U = 8;
+  columns(cuts, runs);  // meanwhile the segments that lie within the CTA
+  if (!cuts) return;
+  // Cut segments whose shares this CTA counted last: a thread takes 4 columns of a head, 8 shares at a time.
+  constexpr int PASSES = (QUADS + NW * 32 - 1) / (NW * 32), U = 8;
   for (int which = 0; which < 2; ++which) {
     for (bool first_level = true;; first_level = false) {
       __syncthreads();
