@@ -52,6 +52,9 @@ constexpr int kTile = 32;            // tokens per tile: two 16-token chunks, ea
 constexpr int kLens = 512;            // sequences whose lengths a CTA keeps in shared memory
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kGroup = 8;            // CTAs whose shares of a segment are joined first, where a segment has many
+// Segments of up to so many tiles are not cut between CTAs.  A CTA then holds up to one segment more or less than its
+// share, about 0.11 us a tile (D 128, 12 warps); joining a segment across CTAs costs about 5 us at the end.
+constexpr int kUncut = 32;
 constexpr float kGuess = -8.f;       // a piece's first reference: fits when its largest weight * V scale is 2^-5 .. 2^7
 constexpr float kUnit = 16777216.f;  // 2^24: what a code's fp16 subnormal stands for, inverted
 
@@ -120,6 +123,7 @@ struct Layout {
   static constexpr int WALK_OFF = QUEUE_OFF + NW * NQ * (int)sizeof(Queued);  // Walk [NW]
   static constexpr int WIN_OFF = WALK_OFF + NW * (int)sizeof(Walk);  // uint64 [NW][32]: where the next 32 chunks' codes are
   static constexpr int SCAN_OFF = WIN_OFF + NW * 256;            // int64 [NW]: tiles of a warp's sequences
+  static constexpr int LONG_OFF = QUEUE_OFF;                     // int [NW]: the longest of them, at the start
   static constexpr int INCL_OFF = WIN_OFF;                       // int64 [NW * 32]: the scan within the warps, at the start
   static constexpr int CONV_OFF = SCAN_OFF + NW * 8;             // CONV [NW]
   static constexpr int JOIN_OFF = WIN_OFF;                       // Run [2 NW], weights and sums: after the tiles
@@ -609,6 +613,7 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
   long long* warp_tiles = reinterpret_cast<long long*>(smem + LY::SCAN_OFF);
+  int* warp_longest = reinterpret_cast<int*>(smem + LY::LONG_OFF);
   long long* incl_s = reinterpret_cast<long long*>(smem + LY::INCL_OFF);
   Piece* pieces = reinterpret_cast<Piece*>(smem + LY::PIECE_OFF);
   int* lens_s = reinterpret_cast<int*>(smem + LY::LENS_OFF);
@@ -630,12 +635,14 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
   auto tiles_of = [](int L) { return (L + kTile - 1) / kTile; };
   {
     long long incl = 0;
+    int longest = 0;
     bool clamped = false;
     for (int i = threadIdx.x * per, e = min(B, i + per); i < e; ++i) {
       const int L = __ldg(p.context_lens + i), Lc = min(max(L, 0), cap);
       clamped |= L != Lc;
       if (i < kLens) lens_s[i] = Lc;
       incl += tiles_of(Lc);
+      longest = max(longest, tiles_of(Lc));
     }
     if (clamped && cta == 0) PA_RECORD_ERROR(PA_ERRBIT_INDEX);
 #pragma unroll
@@ -644,7 +651,11 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
       if (lane >= o) incl += t;
     }
     incl_s[threadIdx.x] = incl;
-    if (lane == 31) warp_tiles[warp] = incl;
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if (lane == 31) {
+      warp_tiles[warp] = incl;
+      warp_longest[warp] = longest;
+    }
   }
   __syncthreads();
   long long wincl = lane < NW ? warp_tiles[lane] : 0;  // tiles up to and with warp `lane`'s sequences
@@ -656,32 +667,46 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
   const long long total = __shfl_sync(0xffffffffu, wincl, NW - 1) * Hkv;
   const long long ctas = min((long long)gridDim.x, total);  // at least one tile for each CTA that takes part
   const bool narrow = (total + 1) * (ctas + 1) < (1ll << 32);
-  long long xs = 0;  // this warp's tiles: [xs, xs + tiles) of the line
-  int tiles = 0;
-  if (cta < ctas) {
-    const long long x0 = udiv(total * cta, ctas, narrow), n = udiv(total * (cta + 1), ctas, narrow) - x0;
-    xs = x0 + n * warp / NW;
-    tiles = (int)(x0 + n * (warp + 1) / NW - xs);
-  }
-  Walk w0 = {};
-  if (tiles > 0) {
-    const long long y = udiv(xs, Hkv, narrow);  // per KV head
+  // The segment and tile at place x of the line.
+  auto find = [&](long long x) {
+    Walk w = {};
+    const long long y = udiv(x, Hkv, narrow);  // per KV head
     const int wsel = __popc(__ballot_sync(0xffffffffu, lane < NW && wincl <= y));
     const long long before = wsel ? __shfl_sync(0xffffffffu, wincl, wsel - 1) : 0;
     const long long li = incl_s[wsel * 32 + lane] + before;
     const int tsel = __popc(__ballot_sync(0xffffffffu, li <= y));
     long long pre = tsel ? __shfl_sync(0xffffffffu, li, tsel - 1) : before;
-    w0.b = (wsel * 32 + tsel) * per;
-    for (;; ++w0.b) {
-      w0.L = len_of(w0.b);
-      if (pre + tiles_of(w0.L) > y) break;
-      pre += tiles_of(w0.L);
+    w.b = (wsel * 32 + tsel) * per;
+    for (;; ++w.b) {
+      w.L = len_of(w.b);
+      if (pre + tiles_of(w.L) > y) break;
+      pre += tiles_of(w.L);
     }
-    const long long in_seq = xs - pre * Hkv;
-    w0.g = (int)udiv(in_seq, tiles_of(w0.L), narrow);
-    w0.t = (int)(in_seq - (long long)w0.g * tiles_of(w0.L));
-    w0.seg_start = xs - w0.t;
+    const long long in_seq = x - pre * Hkv;
+    w.g = (int)udiv(in_seq, tiles_of(w.L), narrow);
+    w.t = (int)(in_seq - (long long)w.g * tiles_of(w.L));
+    w.seg_start = x - w.t;
+    return w;
+  };
+  long long xs = 0;  // this warp's tiles: [xs, xs + tiles) of the line
+  int tiles = 0;
+  if (cta < ctas) {
+    long long x0 = udiv(total * cta, ctas, narrow), x1 = udiv(total * (cta + 1), ctas, narrow);
+    const int longest = __reduce_max_sync(0xffffffffu, lane < NW ? warp_longest[lane] : 0);
+    if (longest <= kUncut) {  // move the cuts to the nearest ends of segments
+      auto nearest = [&](long long x) {
+        if (x == 0 || x == total) return x;
+        const Walk w = find(x);
+        return 2 * w.t < tiles_of(w.L) ? w.seg_start : w.seg_start + tiles_of(w.L);
+      };
+      x0 = nearest(x0);
+      x1 = nearest(x1);
+    }
+    xs = x0 + (x1 - x0) * warp / NW;
+    tiles = (int)(x0 + (x1 - x0) * (warp + 1) / NW - xs);
   }
+  Walk w0 = {};
+  if (tiles > 0) w0 = find(xs);
   __syncthreads();  // the scans are done with: the windows take their place
 
   // ---- what this lane copies of a tile: of each chunk's codes the 16-byte units lane, lane + 32, .. (K and V
