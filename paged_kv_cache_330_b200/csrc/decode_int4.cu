@@ -6,8 +6,9 @@
 // hold 256.  At that size the work per byte, not HBM, is what has to be kept small, so the kernel is built
 // around warps that never wait for one another.
 //
-// Work split.  A segment is one (sequence, KV head), cut into tiles of 32 tokens; all segments end to end form
-// one line of T tiles.  CTA c takes tiles [T c / n, T (c+1) / n), its warps equal parts of that.  Every warp
+// Work split.  A segment is one (sequence, KV head), cut into tiles of 32 tokens.  On a line of all segments end to
+// end, a segment takes kStart places for what starting and ending it costs, then a place per tile.  CTA c takes places
+// [T c / n, T (c+1) / n) of T (moved to the ends of segments where these are short), its warps equal parts of that.  Every warp
 // walks its own part: it looks its blocks up, brings its tiles into a ring of its own with asynchronous 16-byte
 // copies (cp.async, nine a lane per tile; no other warp involved) and keeps the softmax state and the output of
 // the current segment in registers.  Bulk copies were measured first: one instruction per copy, but each of a
@@ -49,6 +50,7 @@ namespace {
 using namespace pa;
 
 constexpr int kTile = 32;            // tokens per tile: two 16-token chunks, each within one block
+constexpr int kStart = 1;             // what a segment costs besides its tiles, in tiles
 constexpr int kLens = 512;            // sequences whose lengths a CTA keeps in shared memory
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kGroup = 8;            // CTAs whose shares of a segment are joined first, where a segment has many
@@ -90,15 +92,14 @@ struct Piece {
 struct Queued {
   int b, g, L, t0;      // sequence, KV head, length, first tile
   long long seg_start;  // where the segment starts on the line
-  long long pad;
+  int end, pad;         // where the piece ends
 };
 // The walk of a warp between two windows of block lookups (kept in shared memory: it is looked at once in 16 tiles).
 struct Walk {
   int b, g, L, t;       // segment, its length, next tile
-  int end, left;        // where the piece ends, and the tiles that follow it
-  int filed, pad;       // pieces filed
-  long long seg_start;
-  long long pad2;
+  int end, pad;         // where the piece ends
+  long long seg_start;  // where the segment starts on the line, and where the warp's part of the line ends
+  long long line_end;
 };
 
 // Pieces of one segment within a CTA, for the joining step.
@@ -121,7 +122,7 @@ struct Layout {
   static constexpr int NQ = NS + 2;                              // pieces filed and not done: NS stages' and one more
   static constexpr int QUEUE_OFF = PIECE_OFF + NW * 2 * (int)sizeof(Piece);  // Queued [NW][NQ]
   static constexpr int WALK_OFF = QUEUE_OFF + NW * NQ * (int)sizeof(Queued);  // Walk [NW]
-  static constexpr int WIN_OFF = WALK_OFF + NW * (int)sizeof(Walk);  // uint64 [NW][32]: where the next 32 chunks' codes are
+  static constexpr int WIN_OFF = (WALK_OFF + NW * (int)sizeof(Walk) + 15) / 16 * 16;  // uint64 [NW][32]: where the next 32 chunks' codes are
   static constexpr int SCAN_OFF = WIN_OFF + NW * 256;            // int64 [NW]: tiles of a warp's sequences
   static constexpr int LONG_OFF = QUEUE_OFF;                     // int [NW]: the longest of them, at the start
   static constexpr int INCL_OFF = WIN_OFF;                       // int64 [NW * 32]: the scan within the warps, at the start
@@ -140,7 +141,7 @@ struct Layout {
     const int unit = word >> 2;
     return row * ROWB + ((ROWB == 64 ? unit ^ (row >> 1 & 3) : unit ^ (row >> 2 & 1)) << 4) + (word & 3) * 4;
   }
-  static_assert(STAGE % 128 == 0 && sizeof(Piece) % 8 == 0 && sizeof(Queued) == 32 && sizeof(Walk) == 48 && PIECE_OFF % 16 == 0 && QUEUE_OFF % 16 == 0 &&
+  static_assert(STAGE % 128 == 0 && sizeof(Piece) % 8 == 0 && sizeof(Queued) == 32 && sizeof(Walk) == 40 && PIECE_OFF % 16 == 0 && QUEUE_OFF % 16 == 0 &&
                     WIN_OFF % 16 == 0 && CONV_OFF % 16 == 0 && CONV % 16 == 0,
                 "alignment");
 };
@@ -633,6 +634,7 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
   const int per = (B + NW * 32 - 1) / (NW * 32);
   auto len_of = [&](int i) { return i < kLens ? lens_s[i] : min(max(__ldg(p.context_lens + i), 0), cap); };
   auto tiles_of = [](int L) { return (L + kTile - 1) / kTile; };
+  auto places_of = [](int L) { return L > 0 ? (L + kTile - 1) / kTile + kStart : 0; };
   {
     long long incl = 0;
     int longest = 0;
@@ -641,7 +643,7 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
       const int L = __ldg(p.context_lens + i), Lc = min(max(L, 0), cap);
       clamped |= L != Lc;
       if (i < kLens) lens_s[i] = Lc;
-      incl += tiles_of(Lc);
+      incl += places_of(Lc);
       longest = max(longest, tiles_of(Lc));
     }
     if (clamped && cta == 0) PA_RECORD_ERROR(PA_ERRBIT_INDEX);
@@ -658,16 +660,16 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
     }
   }
   __syncthreads();
-  long long wincl = lane < NW ? warp_tiles[lane] : 0;  // tiles up to and with warp `lane`'s sequences
+  long long wincl = lane < NW ? warp_tiles[lane] : 0;  // places (per KV head) up to and with warp `lane`'s sequences
 #pragma unroll
   for (int o = 1; o < NW; o <<= 1) {
     const long long t = __shfl_up_sync(0xffffffffu, wincl, o);
     if (lane >= o) wincl += t;
   }
   const long long total = __shfl_sync(0xffffffffu, wincl, NW - 1) * Hkv;
-  const long long ctas = min((long long)gridDim.x, total);  // at least one tile for each CTA that takes part
+  const long long ctas = min((long long)gridDim.x, total);
   const bool narrow = (total + 1) * (ctas + 1) < (1ll << 32);
-  // The segment and tile at place x of the line.
+  // The segment at place x of the line, and the tile (the segment's first one, if x is one of its kStart places).
   auto find = [&](long long x) {
     Walk w = {};
     const long long y = udiv(x, Hkv, narrow);  // per KV head
@@ -679,17 +681,28 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
     w.b = (wsel * 32 + tsel) * per;
     for (;; ++w.b) {
       w.L = len_of(w.b);
-      if (pre + tiles_of(w.L) > y) break;
-      pre += tiles_of(w.L);
+      if (pre + places_of(w.L) > y) break;
+      pre += places_of(w.L);
     }
     const long long in_seq = x - pre * Hkv;
-    w.g = (int)udiv(in_seq, tiles_of(w.L), narrow);
-    w.t = (int)(in_seq - (long long)w.g * tiles_of(w.L));
-    w.seg_start = x - w.t;
+    w.g = (int)udiv(in_seq, places_of(w.L), narrow);
+    const int place = (int)(in_seq - (long long)w.g * places_of(w.L));
+    w.seg_start = x - place;
+    w.t = max(0, place - kStart);
     return w;
   };
-  long long xs = 0;  // this warp's tiles: [xs, xs + tiles) of the line
-  int tiles = 0;
+  // The next segment in line (sequences without tokens have none).
+  auto step_on = [&](Walk& w) {
+    w.seg_start += places_of(w.L);
+    w.t = 0;
+    if (++w.g == p.num_kv_heads) {
+      w.g = 0;
+      do w.L = len_of(++w.b);
+      while (w.L == 0 && w.b < p.batch - 1);
+    }
+  };
+  Walk w0 = {};  // this warp's part of the line: from w0 to w0.line_end
+  bool any = false;
   if (cta < ctas) {
     long long x0 = udiv(total * cta, ctas, narrow), x1 = udiv(total * (cta + 1), ctas, narrow);
     const int longest = __reduce_max_sync(0xffffffffu, lane < NW ? warp_longest[lane] : 0);
@@ -697,16 +710,19 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
       auto nearest = [&](long long x) {
         if (x == 0 || x == total) return x;
         const Walk w = find(x);
-        return 2 * w.t < tiles_of(w.L) ? w.seg_start : w.seg_start + tiles_of(w.L);
+        return 2 * (x - w.seg_start) < places_of(w.L) ? w.seg_start : w.seg_start + places_of(w.L);
       };
       x0 = nearest(x0);
       x1 = nearest(x1);
     }
-    xs = x0 + (x1 - x0) * warp / NW;
-    tiles = (int)(x0 + (x1 - x0) * (warp + 1) / NW - xs);
+    const long long xs = x0 + (x1 - x0) * warp / NW, xe = x0 + (x1 - x0) * (warp + 1) / NW;
+    if (xs < xe) {
+      w0 = find(xs);
+      w0.line_end = xe;
+      // a part that ends in a segment's kStart places, or starts behind its last tile, may hold no tile of it
+      any = w0.t < xe - w0.seg_start - kStart;
+    }
   }
-  Walk w0 = {};
-  if (tiles > 0) w0 = find(xs);
   __syncthreads();  // the scans are done with: the windows take their place
 
   // ---- what this lane copies of a tile: of each chunk's codes the 16-byte units lane, lane + 32, .. (K and V
@@ -726,18 +742,17 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
   Walk* walk = reinterpret_cast<Walk*>(smem + LY::WALK_OFF) + warp;
   const ulonglong2* win_at = nullptr;  // the next tile's two chunks
   int win_left = 0;                    // tiles the window still holds
+  int filed = 0;                       // pieces filed
 
   auto file_piece = [&](Walk& w) {
-    const int nt = tiles_of(w.L);
-    w.end = min(nt, w.t + w.left);
-    w.left -= w.end - w.t;
+    w.end = (int)min((long long)tiles_of(w.L), w.line_end - w.seg_start - kStart);
     if (lane == 0) {
-      Queued& q = queue[w.filed % LY::NQ];
+      Queued& q = queue[filed % LY::NQ];
       *reinterpret_cast<int4*>(&q) = make_int4(w.b, w.g, w.L, w.t);
       q.seg_start = w.seg_start;
+      q.end = w.end;
     }
-    ++w.filed;
-    w.seg_start += nt;  // empty sequences take no room on the line: the next segment follows at once
+    ++filed;
   };
   auto q_rows = [&](int b, int kvh) {
     return reinterpret_cast<const uint8_t*>(p.q) + ((size_t)b * p.num_q_heads + (size_t)kvh * G) * D * 2;
@@ -745,7 +760,7 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
   auto bring_q = [&](const Walk& w) {  // of the piece filed last, with its first tile
     if constexpr (LY::QS) {
       const uint8_t* src = q_rows(w.b, w.g);
-      const uint32_t dst = smem_u32(smem + LY::QS_OFF + (warp * LY::NQ + (w.filed - 1) % LY::NQ) * LY::QB);
+      const uint32_t dst = smem_u32(smem + LY::QS_OFF + (warp * LY::NQ + (filed - 1) % LY::NQ) * LY::QB);
       for (int i = lane; i < LY::QB / 16; i += 32) cp_async16(dst + i * 16, src + i * 16);
     }
   };
@@ -772,19 +787,15 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
   };
   auto next_window = [&]() {
     Walk w = *walk;
-    if (w.t == w.end) {  // the next segment; sequences without tokens have no tiles
-      w.t = 0;
-      if (++w.g == p.num_kv_heads) {
-        w.g = 0;
-        do w.L = len_of(++w.b);
-        while (w.L == 0 && w.b < p.batch - 1);
-      }
+    if (w.t == w.end) {
+      if (w.seg_start + places_of(w.L) + kStart >= w.line_end) return;  // no tile of the next segment is this warp's
+      step_on(w);
       file_piece(w);
       bring_q(w);
     }
     look_up(w);
   };
-  auto bring = [&](uint32_t stage, bool more) {  // the walk's next tile into the stage at this shared address
+  auto bring = [&](uint32_t stage) {  // the walk's next tile into the stage at this shared address
     const ulonglong2 off = *win_at++;
     const uint8_t* k0 = kbase + off.x;
     const uint8_t* v0 = k0 + p.v_codes;
@@ -805,10 +816,9 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
     }
     if (par_run < 4 && (two || !(par_run & 1)))
       cp_async16(stage + par_dst, par_base + (((par_run & 1) ? off.y : off.x) >> 3));
-    if (--win_left == 0 && more) next_window();
+    if (--win_left == 0) next_window();
   };
-  if (tiles > 0) {
-    w0.left = tiles;
+  if (any) {
     file_piece(w0);
     look_up(w0);
   }
@@ -816,10 +826,10 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
   // The cache, q and the output may be in use by the preceding kernel (programmatic dependent launch; lengths and
   // block tables are not its outputs): wait for it before the first load of them and before any write.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (tiles > 0) bring_q(w0);
+  if (any) bring_q(w0);
 #pragma unroll
   for (int s = 0; s < NS; ++s) {
-    if (s < tiles) bring(ring + s * LY::STAGE, s + 1 < tiles);
+    if (win_left) bring(ring + s * LY::STAGE);
     cp_async_commit();
   }
   // sequences without a token: zeros, and a log-sum-exp of -inf
@@ -833,15 +843,14 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
 
   // ---- pieces and their tiles
   S st;
-  int stage_at = 0, to_bring = tiles - NS;  // byte offset of the current stage; tiles still to be brought in
-  for (int todo = tiles, piece = 0; todo > 0; ++piece) {
-    const Queued& d = queue[piece % LY::NQ];  // written before a warp barrier that this warp has passed
+  int stage_at = 0;  // byte offset of the current stage
+  for (int piece = 0; piece < filed; ++piece) {  // a piece's successor is filed before its last tile is done
+    const Queued& d = queue[piece % LY::NQ];     // written before a warp barrier that this warp has passed
     int rem;  // tokens of the segment from the current tile on
     {
       const int4 e = *reinterpret_cast<const int4*>(&d);
+      int m = d.end - e.w;  // the piece's tiles
       rem = e.z - e.w * kTile;
-      int m = min((rem + kTile - 1) / kTile, todo);   // the piece's tiles
-      todo -= m;
       if constexpr (LY::QS) {
         cp_async_wait<NS - 1>();
         __syncwarp();
@@ -855,8 +864,7 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
         st.template tile<LY>(smem + LY::RING_OFF + warp * LY::RING + stage_at, smem + LY::CONV_OFF + warp * LY::CONV, rem,
                              lane);
         __syncwarp();
-        if (to_bring > 0) bring(ring + stage_at, to_bring > 1);
-        --to_bring;
+        if (win_left) bring(ring + stage_at);
         cp_async_commit();
         stage_at = stage_at == (NS - 1) * LY::STAGE ? 0 : stage_at + LY::STAGE;
         rem -= kTile;
@@ -891,7 +899,7 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
             p.lse[(size_t)b * p.num_q_heads + (size_t)kvh * G + h] = (st.R[n][e] + __log2f(st.l[n][e])) * kLn2;
         }
     } else {
-      const int which = todo == 0;  // the warp's last piece lies in its ring, which is done with
+      const int which = piece + 1 == filed;  // the warp's last piece lies in its ring, which is done with
       float* part = reinterpret_cast<float*>(which ? smem + LY::RING_OFF + warp * LY::RING
                                                    : smem + LY::PART_OFF + warp * LY::PART);
 #pragma unroll
@@ -1037,8 +1045,9 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
   if (lane < 2 && (lane == 0 ? cut0 : cut1)) {
     const Piece& mine = pieces[__ffs(run_s[lane == 0 ? 0 : runs - 1].mask) - 1];
     seg = (size_t)mine.b * Hkv + mine.g;
-    c0 = (int)udiv((mine.seg_start + 1) * ctas - 1, total, narrow);
-    n_sh = (int)udiv((mine.seg_start + mine.nt) * ctas - 1, total, narrow) - c0 + 1;
+    const long long tile0 = mine.seg_start + kStart;
+    c0 = (int)udiv((tile0 + 1) * ctas - 1, total, narrow);
+    n_sh = (int)udiv((tile0 + mine.nt) * ctas - 1, total, narrow) - c0 + 1;
   }
   // A segment with many shares is joined by groups of kGroup CTAs first: one SM reads shares at little more than
   // 100 GB/s.
