@@ -61,18 +61,19 @@ __device__ __forceinline__ uint4 pack8(const float* x) {
                     Elt<DT>::from_f2(x[6], x[7]));
 }
 
-// 8 values -> a word of 8 codes; x becomes the values that the codes stand for (unrounded).  Clamping before rounding
-// gives what rounding first gives (the ends are whole), and keeps the sum with 1.5 * 2^23 exact but for its one
-// rounding, to a whole number, half to even; the code is then in that sum's low bits.
-__device__ __forceinline__ uint32_t encode8(float* x, float s, float z, float inv) {
+// 8 values -> a word of 8 codes, code = clamp(rint(x * inv - shift), 0, 15); HELD: x becomes the values s * (code + z)
+// that they stand for (unrounded).  Clamping before rounding gives what rounding first gives (the ends are whole), and
+// keeps the sum with 1.5 * 2^23 exact but for its one rounding, to a whole number, half to even; the code is then in
+// that sum's low bits.
+template <bool HELD>
+__device__ __forceinline__ uint32_t encode8(float* x, float s, float z, float inv, float shift) {
   constexpr float kWhole = 12582912.f;
   uint32_t word = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float t = fminf(fmaxf(__fsub_rn(__fmul_rn(x[i], inv), z), 0.f), 15.f);
-    const float m = __fadd_rn(inv == 0.f ? 0.f : t, kWhole);
+    const float m = __fadd_rn(fminf(fmaxf(__fsub_rn(__fmul_rn(x[i], inv), shift), 0.f), 15.f), kWhole);
     word += (__float_as_uint(m) - __float_as_uint(kWhole)) << (4 * i);
-    x[i] = __fmul_rn(s, __fadd_rn(__fsub_rn(m, kWhole), z));
+    if (HELD) x[i] = __fmul_rn(s, __fadd_rn(__fsub_rn(m, kWhole), z));
   }
   return word;
 }
@@ -101,7 +102,7 @@ struct WriteArgs {
   uint4* v_out;
   int64_t num_slots, max_position;
   int total;  // threads' items: tokens * (hq + 2 * hkv) * D / 16
-  int hq, hkv, block_size;
+  int hq, hkv, bs_shift;  // block sizes are powers of two
 };
 
 // Items: per token hq rows of q (rotary form), hkv rows of k, hkv rows of v; D/16 neighbouring threads a row.
@@ -212,9 +213,21 @@ __global__ void __launch_bounds__(256) write_kv_int4_kernel(const WriteArgs a) {
       inv2 = __shfl_sync(0xffffffffu, quot, 3, TPR);
     }
     if (!live || isq) return;
-    const uint32_t w1 = encode8(x1, s1, z1, inv1), w2 = encode8(x2, s2, z2, inv2);
-    const int64_t blk = slot / a.block_size;
-    const int64_t crow = (blk * a.hkv + h) * a.block_size + (slot - blk * a.block_size);
+    // where 1 / s is taken as 0 every code is to be 0: the shift 1 sees to it
+    const float shift1 = inv1 == 0.f ? 1.f : z1, shift2 = inv2 == 0.f ? 1.f : z2;
+    uint4* held = isv ? a.v_out : a.k_out;
+    uint32_t w1, w2;
+    if (held) {
+      w1 = encode8<true>(x1, s1, z1, inv1, shift1);
+      w2 = encode8<true>(x2, s2, z2, inv2, shift2);
+      st_v4(held + vec, pack8<DT>(x1));
+      st_v4(held + vec + TPR, pack8<DT>(x2));
+    } else {
+      w1 = encode8<false>(x1, s1, z1, inv1, shift1);
+      w2 = encode8<false>(x2, s2, z2, inv2, shift2);
+    }
+    const int64_t blk = slot >> a.bs_shift;
+    const int64_t crow = ((blk * a.hkv + h) << a.bs_shift) + (slot & ((1 << a.bs_shift) - 1));
     uint32_t* cw = reinterpret_cast<uint32_t*>(isv ? a.vc : a.kc) + crow * (D / 8);
     uint32_t* pw = (isv ? a.vp : a.kp) + crow * NG;
     if constexpr (NG == 2) {
@@ -224,11 +237,6 @@ __global__ void __launch_bounds__(256) write_kv_int4_kernel(const WriteArgs a) {
       cw[j + 4] = w2;
     }
     if (!odd && j < 2 * NG) pw[j >> 1] = pword;
-    uint4* held = isv ? a.v_out : a.k_out;
-    if (held) {
-      st_v4(held + vec, pack8<DT>(x1));
-      st_v4(held + vec + TPR, pack8<DT>(x2));
-    }
   }
 }
 
@@ -269,13 +277,18 @@ __global__ void __launch_bounds__(256) copy_blocks_int4_kernel(const int32_t* __
   }
 }
 
-// 8 codes of a word -> values s * (code + z), rounded to the type.
+// 8 codes of a word -> values s * (code + z), rounded to the type.  A code becomes a float by one permute, as the low
+// byte of 2^23.
 template <int DT>
 __device__ __forceinline__ uint4 expand8(uint32_t w, uint32_t param) {
   const float2 p = Elt<DT>::to_f2(param);
+  const uint32_t even = w & 0x0f0f0f0fu, odd = (w >> 4) & 0x0f0f0f0fu;
   float x[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(p.x, __fadd_rn((float)((w >> (4 * i)) & 15u), p.y));
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t m = __byte_perm((i & 1) ? odd : even, 0x4B000000u, 0x7440u | (uint32_t)(i >> 1));
+    x[i] = __fmul_rn(p.x, __fadd_rn(__fsub_rn(__uint_as_float(m), 8388608.f), p.y));
+  }
   return pack8<DT>(x);
 }
 
@@ -383,7 +396,7 @@ extern "C" int pa_write_kv_int4(const void* k, const void* v, const int64_t* slo
   a.num_slots = (int64_t)num_blocks * block_size;
   a.total = (int)total;
   a.hkv = num_kv_heads;
-  a.block_size = block_size;
+  a.bs_shift = __builtin_ctz((unsigned)block_size);
   return launch_write<false>(a, head_dim, dtype, (cudaStream_t)stream);
 }
 
@@ -425,7 +438,7 @@ extern "C" int pa_rope_write_kv_int4(const void* q, void* q_out, const void* k, 
   a.total = (int)total;
   a.hq = num_q_heads;
   a.hkv = num_kv_heads;
-  a.block_size = block_size;
+  a.bs_shift = __builtin_ctz((unsigned)block_size);
   return launch_write<true>(a, head_dim, dtype, (cudaStream_t)stream);
 }
 
