@@ -8,15 +8,15 @@
 //
 // Work split.  A segment is one (sequence, KV head), cut into tiles of 32 tokens.  On a line of all segments end to
 // end, a segment takes kStart places for what starting and ending it costs, then a place per tile.  CTA c takes places
-// [T c / n, T (c+1) / n) of T (moved to the ends of segments where these are short), its warps equal parts of that.  Every warp
-// walks its own part: it looks its blocks up, brings its tiles into a ring of its own with asynchronous 16-byte
-// copies (cp.async, nine a lane per tile; no other warp involved) and keeps the softmax state and the output of
-// the current segment in registers.  Bulk copies were measured first: one instruction per copy, but each of a
+// [T c / n, T (c+1) / n) of T (moved to the ends of segments where these are short), its warps equal parts of that.
+// Every warp walks its own part: it looks its blocks up, brings its tiles into a ring of its own with asynchronous
+// 16-byte copies (cp.async, nine a lane per tile; no other warp involved) and keeps the softmax state and the output
+// of the current segment in registers.  Bulk copies were measured first: one instruction per copy, but each of a
 // tile's eight takes a turn of its own through the uniform path, 200 of the 700 instructions of a tile.
 // What a warp holds of a segment is a piece: a whole segment is written out at once, a partial one goes to
 // shared memory, and after the one barrier at the end of the tiles the pieces of a segment are joined, first
 // within the CTA, then, for the at most two segments that a CTA shares with its neighbours, through the
-// workspace by the CTA that counts last (a counter per segment, no waiting).  The joining order is the order of
+// workspace by the CTA that counts last (a counter per cut segment, no waiting).  The joining order is the order of
 // the line, so results do not depend on timing.
 //
 // Mathematics.  Products run on mma.m16n8k16 (fp16 in, fp32 out) with tokens (scores) or columns (PV) as the 16
@@ -50,13 +50,16 @@ namespace {
 using namespace pa;
 
 constexpr int kTile = 32;            // tokens per tile: two 16-token chunks, each within one block
-constexpr int kStart = 1;             // what a segment costs besides its tiles, in tiles
-constexpr int kLens = 512;            // sequences whose lengths a CTA keeps in shared memory
+constexpr int kStart = 1;            // what a segment costs besides its tiles, in tiles
+constexpr int kLens = 512;           // sequences whose lengths a CTA keeps in shared memory
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kGroup = 8;            // CTAs whose shares of a segment are joined first, where a segment has many
 // Segments of up to so many tiles are not cut between CTAs.  A CTA then holds up to one segment more or less than its
 // share, about 0.11 us a tile (D 128, 12 warps); joining a segment across CTAs costs about 5 us at the end.
 constexpr int kUncut = 32;
+// CTAs of a grid, at most.  The counters' room is this large whatever the sizes, so that a workspace serves calls of
+// any sizes in turn: nothing of one call's results lies where the next one counts.
+constexpr int kMaxGrid = 1024;
 constexpr float kGuess = -8.f;       // a piece's first reference: fits when its largest weight * V scale is 2^-5 .. 2^7
 constexpr float kUnit = 16777216.f;  // 2^24: what a code's fp16 subnormal stands for, inverted
 
@@ -70,14 +73,18 @@ struct Params {
   long long v_params;
   const int32_t* block_tables;
   const int32_t* context_lens;
-  int* ws_cnt;   // [batch * Hkv] CTAs that have added their share of a segment (zero between calls)
-  int* ws_grp;   // [slots] the same within a group of CTAs (zero between calls)
+  int* ws_cnt;   // [3 kMaxGrid], zero between calls, see counter_of
   float* ws_r;   // [slots][G] reference R of a share
   float* ws_l;   // [slots][G]
   float* ws_o;   // [slots][G][D]
   int max_blocks_per_seq, batch, num_q_heads, num_kv_heads, block_size, num_blocks;
   float scale_log2;
 };
+
+// Which counter a cut segment whose first tile is CTA c0's counts its shares with (a CTA holds the first tile of one cut
+// segment at most), and which one the group of its CTAs from gf on (a CTA holds a later share of one segment at most).
+__device__ __forceinline__ int counter_of(int c0) { return c0; }
+__device__ __forceinline__ int group_counter_of(int c0, int gf) { return gf == c0 ? kMaxGrid + gf : 2 * kMaxGrid + gf; }
 
 enum : int { F_VALID = 1, F_HEAD = 2, F_TAIL = 4 };
 
@@ -179,11 +186,6 @@ __device__ __forceinline__ uint32_t as_u32(__half2 a) { return *reinterpret_cast
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
-}
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 __device__ __forceinline__ float rows_max(float v) {  // over the 8 lanes that share a column
@@ -1053,7 +1055,7 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
   // 100 GB/s.
   const int gf = max(c0, cta / kGroup * kGroup);
   const bool grouped = n_sh > 2 * kGroup;
-  int* cnt = grouped ? p.ws_grp + seg + gf : p.ws_cnt + seg;
+  int* cnt = p.ws_cnt + (grouped ? group_counter_of(c0, gf) : counter_of(c0));
   int n = grouped ? min(c0 + n_sh, (cta / kGroup + 1) * kGroup) - gf : n_sh;  // shares to join now, from slot0 on
   size_t slot0 = seg + (grouped ? gf : c0), slots = slot0;
   int step = 1;
@@ -1141,23 +1143,27 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
       step = kGroup;
       n = (c0 + n_sh - 1) / kGroup - c0 / kGroup + 1;
       __syncthreads();
-      if (warp == 0 && lane == which) done_s[lane] = count_last(p.ws_cnt + seg, n);
+      if (warp == 0 && lane == which) done_s[lane] = count_last(p.ws_cnt + counter_of(c0), n);
     }
   }
 }
 
 // ------------------------------------------------------------------ host side
-constexpr int kWarps = 12;  // consumer warps of a CTA (G 16: 8)
+// Warps of a CTA (one CTA fills an SM) and stages of each warp's ring.  D 128, G <= 8: 12 warps of 168 registers; 16 warps
+// of 128 need 590 instructions a tile instead of 522 (values kept and fetched again): 64 sequences of 4096 to 8192
+// tokens, 64 heads, take 92.9 us with 16, 89.5 with 12, 101 with 10, 107 with 8.  D 64 fits 16 (27.4 against 28.6 us,
+// 64 sequences of 500 to 8000).  G 16 holds two column tiles, 250 registers.  A third stage changes nothing.
+constexpr int kWarps = 12;
 
 template <int D, int G>
 struct Shape {
-  static constexpr int NW = G == 16 ? 8 : kWarps;
+  static constexpr int NW = G == 16 ? 8 : (D == 64 ? 16 : kWarps);
   static constexpr int NS = 2;
 };
 
 struct Plan {
   int grid;
-  size_t off_grp, off_r, off_l, off_o, bytes;
+  size_t off_r, off_l, off_o, bytes;
 };
 
 bool make_plan(int batch, int Hq, int Hkv, int D, int max_context_len, int num_partitions, Plan* pl) {
@@ -1176,11 +1182,10 @@ bool make_plan(int batch, int Hq, int Hkv, int D, int max_context_len, int num_p
     const int64_t up = std::min(sms / segs, (grid + segs - 1) / segs) * segs;
     if (up >= grid || up * 20 >= grid * 19) grid = up;
   }
-  pl->grid = num_partitions ? num_partitions : (int)grid;
+  pl->grid = std::min(num_partitions ? num_partitions : (int)grid, kMaxGrid);
   auto align256 = [](size_t x) { return (x + 255) & ~size_t(255); };
   const size_t slots = (size_t)batch * Hkv + pl->grid;
-  pl->off_grp = align256((size_t)batch * Hkv * 4);
-  pl->off_r = pl->off_grp + align256(slots * 4);
+  pl->off_r = 3 * kMaxGrid * 4;
   pl->off_l = pl->off_r + align256(slots * G * 4);
   pl->off_o = pl->off_l + align256(slots * G * 4);
   pl->bytes = pl->off_o + align256(slots * G * D * 4);
@@ -1280,7 +1285,6 @@ extern "C" int pa_decode_int4(const void* q, const void* k_codes, const void* v_
   p.block_tables = block_tables;
   p.context_lens = context_lens;
   p.ws_cnt = reinterpret_cast<int*>(ws);
-  p.ws_grp = reinterpret_cast<int*>(ws + pl.off_grp);
   p.ws_r = reinterpret_cast<float*>(ws + pl.off_r);
   p.ws_l = reinterpret_cast<float*>(ws + pl.off_l);
   p.ws_o = reinterpret_cast<float*>(ws + pl.off_o);

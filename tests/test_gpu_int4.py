@@ -388,6 +388,28 @@ def test_decode_int4_bad_block_sets_index_bit():
 
 
 # ------------------------------------------------------------------------------------------ streams, graphs, workspaces
+def test_decode_int4_one_workspace_for_calls_of_all_sizes():
+    """A workspace zero-filled once and used by calls of other batches, heads, dimensions and work splits in turn, each
+    with segments cut between CTAs: every call's result is that of a fresh workspace, bit for bit."""
+    calls = []
+    for seed, (lens, Hq, Hkv, D, ns) in enumerate([
+            ([9000, 40], 8, 1, 128, 0), ([700] * 40, 16, 8, 64, 37), ([20000], 16, 1, 64, 300),
+            ([3000, 0, 5, 1200] * 30, 8, 4, 128, 0), ([2000] * 3, 4, 2, 64, 1000), ([9000, 40], 8, 1, 128, 0)]):
+        wl = make_custom(seed=50 + seed, lens=lens, num_q_heads=Hq, num_kv_heads=Hkv, head_dim=D, block_size=16)
+        _, cache, bt, ln = _pool_step(wl)
+        dev = torch.from_numpy(bt).cuda(), torch.from_numpy(ln).cuda()
+        calls.append((wl.q.cuda(), cache, *dev, int(ln.max()), wl.scale, ns,
+                      pa.decode_int4_plan(len(lens), Hq, Hkv, D, int(ln.max()), ns)[2]))
+    ws = torch.zeros(max(c[-1] for c in calls), dtype=torch.uint8, device="cuda")
+    for again in range(2):
+        for i, (q, cache, bt, ln, top, scale, ns, need) in enumerate(calls):
+            got, got_lse, want, want_lse = (torch.empty_like(q), torch.empty(q.shape[:2], device="cuda"),
+                                            torch.empty_like(q), torch.empty(q.shape[:2], device="cuda"))
+            pa.decode_int4(q, *cache, bt, ln, top, scale, out=got, lse=got_lse, workspace=ws, num_partitions=ns)
+            pa.decode_int4(q, *cache, bt, ln, top, scale, out=want, lse=want_lse, num_partitions=ns)
+            assert torch.equal(got, want) and torch.equal(got_lse, want_lse), (again, i)
+
+
 def test_decode_int4_graph_replay_and_side_stream():
     """Write and decode captured once on a side stream and replayed with new inputs: the eager calls' bits; the
     workspace ends zeroed; two graphs with a workspace each, replayed in turn."""

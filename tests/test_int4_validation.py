@@ -91,9 +91,11 @@ def test_decode_int4_plan():
     for B, Hq, Hkv, D, L in ((4, 4, 4, 64, 64), (128, 16, 8, 128, 1024), (64, 64, 8, 128, 8192), (1, 32, 2, 128, 100001)):
         grid, pieces, ws = pa.decode_int4_plan(B, Hq, Hkv, D, L)
         assert 1 <= grid and pieces == B * Hkv + grid
-        assert ws >= 4 * (B * Hkv + pieces) + pieces * (Hq // Hkv) * (D + 2) * 4
+        assert ws >= 3 * 4 * 1024 + pieces * (Hq // Hkv) * (D + 2) * 4
         assert pa.lib.pa_decode_int4_workspace_size(B, Hq, Hkv, D, L, 0) == ws
     assert pa.decode_int4_plan(4, 8, 2, 128, 1000, num_partitions=7)[0] == 7
+    assert pa.decode_int4_plan(4, 8, 2, 128, 1000, num_partitions=1 << 30) == pa.decode_int4_plan(
+        4, 8, 2, 128, 1000, num_partitions=1024)
     # a small batch's grid is a multiple of its segments: contexts of one length are cut where CTAs meet, or not at all
     assert pa.decode_int4_plan(1, 16, 8, 128, 300)[0] % 8 == 0
     for bad in ((4, 8, 2, 96, 100), (4, 6, 4, 128, 100), (4, 64, 2, 128, 100), (-1, 8, 2, 128, 100), (4, 8, 2, 128, -1)):
