@@ -468,11 +468,13 @@ def run_ours(args):
     dev = torch.device("cuda", local)
     wl = make_workload(args.workload, seed=None if rank == 0 else 1000 * rank + 1, block_size=args.block_size)
     c = wl.cfg
-    int8 = args.kv == "int8"
+    int8, int4 = args.kv == "int8", args.kv == "int4"
+    if int4 and args.cascade:
+        raise SystemExit("--cascade reads a 16-bit cache")
     _, bt, lens, sm, _ = pa.replay_ops(wl.ops, wl.num_blocks, c["block_size"], wl.free_order, wl.batch)
     maxL = int(lens.max())
     B, Hq, Hkv, D = wl.batch, c["num_q_heads"], c["num_kv_heads"], c["head_dim"]
-    plan = pa.decode_int8_plan if int8 else pa.decode_plan
+    plan = pa.decode_int8_plan if int8 else pa.decode_int4_plan if int4 else pa.decode_plan
     grid, maxp, wsb = plan(B, Hq, Hkv, D, maxL, args.num_partitions)
 
     # device-resident inputs
@@ -503,6 +505,18 @@ def run_ours(args):
 
         def dec(st, x=base, o=out):
             pa.decode_int8(x["q"], kq, vq, ksc, vsc, x["bt"], x["lens"], maxL, wl.scale, out=o, workspace=work,
+                           num_partitions=args.num_partitions, stream=st)
+    elif int4:  # the same, into a fresh INT4 cache
+        cache = [torch.zeros((NB, Hkv, bs, D // 2), dtype=torch.uint8, device=dev) for _ in range(2)]
+        cache += [torch.zeros((NB, Hkv, bs, D // 64, 2), dtype=wl.q.dtype, device=dev) for _ in range(2)]
+        pa.write_kv_int4(wl.k_cache0.to(dev).view(NB * bs, Hkv, D), wl.v_cache0.to(dev).view(NB * bs, Hkv, D),
+                         torch.arange(NB * bs, dtype=torch.int64, device=dev), *cache)
+
+        def wr(st, x=base):
+            pa.write_kv_int4(x["kn"], x["vn"], x["sm"], *cache, stream=st)
+
+        def dec(st, x=base, o=out):
+            pa.decode_int4(x["q"], *cache, x["bt"], x["lens"], maxL, wl.scale, out=o, workspace=work,
                            num_partitions=args.num_partitions, stream=st)
     elif args.cascade:  # shared prefixes read once for all sharers (groups of consecutive sequences)
         kc = wl.k_cache0.to(dev)
@@ -640,6 +654,9 @@ def run_ours(args):
     if int8:  # one byte per element plus one fp32 scale per (token, KV head) row, for K and for V
         kvb = kvb // (2 * D) * (D + 4)
         kvb_logical = kvb_logical // (2 * D) * (D + 4)
+    if int4:  # half a byte per element plus a 16-bit scale and zero point per 64
+        kvb = kvb // (2 * D) * (D // 2 + D // 16)
+        kvb_logical = kvb_logical // (2 * D) * (D // 2 + D // 16)
     (ms_step, e2e_ms, e2e_seq_ms, e2e_graph_ms, dec_avg), (kv_all, kvl_all, seqs_all) = reduce_over_ranks(
         [ms_step, e2e_ms, e2e_seq_ms, e2e_graph_ms, float(statistics.median(dec_ms))], [kvb, kvb_logical, B],
         ws, dev)
@@ -649,7 +666,7 @@ def run_ours(args):
     peak, peak_kind = measured_hbm_peak()
     alg = kvb + io_bytes(wl)
     achieved = alg / (dec_avg * 1e-3) / 1e9
-    tr = NCU_TRAFFIC.get(args.workload + ("_int8" if int8 else "") + ("_cascade" if args.cascade else ""))
+    tr = NCU_TRAFFIC.get(args.workload + ("_" + args.kv if int8 or int4 else "") + ("_cascade" if args.cascade else ""))
     if tr and args.cascade and c["block_size"] != 16:
         tr = None  # captured at block size 16
     traffic = tr["bytes"] if tr and tr.get("src") == kernel_source_hash(tr["files"]) else None
@@ -663,9 +680,10 @@ def run_ours(args):
         line = {
             "metric": METRIC, "value": value, "unit": UNIT, "n_gpus": ws, "steps": K, "warmup": args.warmup,
             "ms_per_step": ms_step, "higher_is_better": True, "scaling": "weak", "vs_baseline": None,
-            "dtype": str(c["dtype"]) + ("+int8 cache" if int8 else ""), "data": "synthetic",
+            "dtype": str(c["dtype"]) + (f"+{args.kv} cache" if int8 or int4 else ""), "data": "synthetic",
             "config": {"workload": WORKLOAD_TEXT.get(args.workload, args.workload), "global_batch": int(seqs_all),
-                       "kv_cache": "int8 codes + fp32 row scales" if int8 else str(c["dtype"]),
+                       "kv_cache": {"int8": "int8 codes + fp32 row scales",
+                                    "int4": "4-bit codes + 16-bit scale and zero point per 64"}.get(args.kv, str(c["dtype"])),
                        "decode": "cascade over shared prefixes" if args.cascade else "per-sequence",
                        "block_size": int(c["block_size"]),
                        "parallelism": f"dp{ws} (independent replicas)", "l2": "inputs larger than L2 (no flush)",
@@ -687,7 +705,7 @@ def run_ours(args):
                                    "how": "copy in, calls, copy out on one stream, step after step"},
                     "graph_replay": {"value": kv_all / (e2e_graph_ms * 1e-3) / 1e9, "ms_per_step": e2e_graph_ms,
                                      "how": "the sequential steps captured in a CUDA graph"}},
-            "roofline": {"bound": "hbm", "kernel": ("pa_decode_int8" if int8 else
+            "roofline": {"bound": "hbm", "kernel": ("pa_decode_" + args.kv if int8 or int4 else
                                                     "pa_decode_cascade (suffix decode + shared-prefix pass)"
                                                     if args.cascade else "pa_decode") +
                          ("" if args.cascade else " (one kernel: gather, attention, split-K merge)"),
@@ -1065,8 +1083,9 @@ def main():
     ap.add_argument("--block-size", type=int, default=None, help="override the workload's block size")
     ap.add_argument("--cascade", action="store_true",
                     help="prefix-shared workload: read each shared prefix once for all sharers (pa_decode_cascade)")
-    ap.add_argument("--kv", choices=["bf16", "int8"], default="bf16",
-                    help="decode workloads: the cache format (int8 = codes + fp32 row scales)")
+    ap.add_argument("--kv", choices=["bf16", "int8", "int4"], default="bf16",
+                    help="decode workloads: the cache format (int8 = codes + fp32 row scales, int4 = 4-bit codes + a "
+                         "16-bit scale and zero point per 64)")
     ap.add_argument("--ref-budget", type=float, default=12.0, help="seconds of oracle time per reference sample")
     ap.add_argument("--ref-seqs", type=int, default=128)
     ap.add_argument("--no-cpu-baseline", action="store_true")
