@@ -22,9 +22,13 @@
 // Mathematics.  Products run on mma.m16n8k16 (fp16 in, fp32 out) with tokens (scores) or columns (PV) as the 16
 // rows and up to 8 heads of the group as the 8 columns; G 16 takes two column tiles.
 //   * Codes enter as fp16 subnormals: a nibble in the low four bits of a half is code * 2^-24, in the next four
-//     code * 2^-20, exactly.  Widening a word of 8 codes is one shift and four ANDs, with no offset to take out
-//     again; the factors 2^24 and 16 sit in the score scale, in q (its odd values enter divided by 16) and in
-//     the final scaling of the output rows.
+//     code * 2^-20, exactly, with no offset to take out again.  Widening a word of 8 codes of V is one shift and four
+//     ANDs; the factors 2^24 and 16 sit in the final scaling of the output rows.  The matrix unit lines products up by
+//     the operands' exponent fields, and that of a subnormal is 2^-14 whatever its value: it cuts a product with a code
+//     at 2^-24 where the products of normal numbers are cut at 2^-34.  With V that is 2^-14 of the largest weight in 16,
+//     less than the weights' own rounding.  With K it would be 2^-14 of the largest q: errors of 2e-5 in scores of
+//     ordinary size, against 2e-7 with all of K's codes 2^4 higher, in bits 4 to 7.  That costs two multiplications a
+//     word, 2 % of the time (128 sequences 23.8 -> 24.5 us, long ones 99 -> 101 us).
 //   * Parameters are converted once per token (lane = token), not once per lane that needs them, and handed round
 //     through shared memory: s_K times the score scale as fp32, s_V as fp32, both z as fp16.
 //   * Scores: s_t = sum_group s_K (sum code q + z_K sum q).  The zero-point part is one more product per group, of z
@@ -62,6 +66,7 @@ constexpr int kUncut = 32;
 constexpr int kMaxGrid = 1024;
 constexpr float kGuess = -8.f;       // a piece's first reference: fits when its largest weight * V scale is 2^-5 .. 2^7
 constexpr float kUnit = 16777216.f;  // 2^24: what a code's fp16 subnormal stands for, inverted
+constexpr float kUnitK = 1048576.f;  // 2^20: the same for K's codes
 
 struct Params {
   const void* q;
@@ -222,19 +227,20 @@ __device__ __forceinline__ bool count_last(int* cnt, int n) {
   return true;
 }
 
+constexpr uint32_t kOnes = 0x3c003c00u;  // fp16 1.0, twice
 constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;  // a nibble of each half, worth 2^-24 and 2^-20
 
 // ------------------------------------------------------------------ a warp's state over one piece
 template <int DT, int D, int G>
 struct State {
   static constexpr int NG = D / 64, KS = D / 16, NT = (G + 7) / 8, WPL = D / 32;  // WPL: K words a lane reads of a row
-  uint32_t qb[NT][KS][2];  // q as B operand (fp16, prescaled; odd values divided by 16)
-  uint32_t qsum[NT][NG];   // B operand of the zero-point product: lanes c = 0 the sum of q over a group, 2^-18 of it in two terms
+  uint32_t qb[NT][KS][2];  // q as B operand (fp16, prescaled)
+  uint32_t qsum[NT][NG];   // B operand of the zero-point product: lanes c = 0 the sum of q over a group, 2^-14 of it in two terms
   float o[NT][KS][4];      // O^T times 2^-24 (rows g) and 2^-20 (rows g + 8), columns heads
   float z[NT][NG][4];      // sum P' z_V (columns heads; all rows alike)
   float l[NT][2];          // this lane's part of sum 2^(x - R)
   float R[NT][2];
-  float qs;                // scale * log2(e) * 2^24 / prescale
+  float qs;                // scale * log2(e) * 2^20 / prescale
   bool fresh;              // some head has met no non-zero V scale yet: its R is not set
 
   // qrows: the group's [G][D] rows of q.  A lane loads just the values its operands hold.
@@ -276,7 +282,7 @@ struct State {
       e = min(60, max(-60, 15 - k));
     }
     const float f = __int_as_float((127 + e) << 23), finv = __int_as_float((127 - e) << 23);
-    qs = scale_log2 * finv * kUnit;
+    qs = scale_log2 * finv * kUnitK;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -287,7 +293,7 @@ struct State {
         for (int m = 0; m < 4; ++m) {
           const float2 v = Elt<DT>::to_f2(w[m]);
           x[2 * m] = v.x * f;
-          x[2 * m + 1] = v.y * f * 0.0625f;
+          x[2 * m + 1] = v.y * f;
         }
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
@@ -302,11 +308,10 @@ struct State {
         for (int i = grp; i < WPL; i += NG)
 #pragma unroll
           for (int s = 0; s < 2; ++s)
-            mma_f16(i == grp && s == 0, acc, 0x00010001u, 0x00010001u, 0x00100010u, 0x00100010u, qb[nt][2 * i + s][0],
-                    qb[nt][2 * i + s][1]);
-        // lane g takes head 8nt + g, which column 2 (g / 2) + g % 2 of any row holds; acc is 2^-24 of the sum
+            mma_f16(i == grp && s == 0, acc, kOnes, kOnes, kOnes, kOnes, qb[nt][2 * i + s][0], qb[nt][2 * i + s][1]);
+        // lane g takes head 8nt + g, which column 2 (g / 2) + g % 2 of any row holds
         const float s0 = __shfl_sync(0xffffffffu, acc[0], g >> 1), s1 = __shfl_sync(0xffffffffu, acc[1], g >> 1);
-        const float sum = ((g & 1) ? s1 : s0) * 64.f, hi = __half2float(__float2half_rn(sum));
+        const float sum = ((g & 1) ? s1 : s0) * (64.f / kUnitK), hi = __half2float(__float2half_rn(sum));
         qsum[nt][grp] = c == 0 ? pack_h2(hi, sum - hi) : 0u;
         z[nt][grp][0] = z[nt][grp][1] = z[nt][grp][2] = z[nt][grp][3] = 0.f;
       }
@@ -423,6 +428,8 @@ struct State {
     __syncwarp();
     // ---- scores relative to R, columns heads 8nt + 2c + {0,1}
     float x[2][NT][4];
+    uint32_t times16;  // a shift by 4 on the multiplier's pipe: the compiler, seeing the 16, would shift twice on the other
+    asm("mov.u32 %0, 16;" : "=r"(times16));
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt) {
       float ks[2][NG];
@@ -448,8 +455,8 @@ struct State {
           const uint32_t a = kc[2 * mt][i] >> (8 * s), b = kc[2 * mt + 1][i] >> (8 * s);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
-            mma_f16(i < NG && s == 0, acc[nt][i % NG], a & kLow, b & kLow, a & kHigh, b & kHigh, qb[nt][2 * i + s][0],
-                    qb[nt][2 * i + s][1]);
+            mma_f16(i < NG && s == 0, acc[nt][i % NG], a * times16 & kHigh, b * times16 & kHigh, a & kHigh, b & kHigh,
+                    qb[nt][2 * i + s][0], qb[nt][2 * i + s][1]);
         }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)

@@ -322,6 +322,24 @@ def test_decode_int4_large_logits():
     assert torch.isfinite(got).all()
 
 
+@pytest.mark.parametrize("D,Hq,Hkv,dtype", [(128, 8, 2, "bf16"), (64, 4, 4, "f16"), (128, 16, 1, "f16")])
+def test_decode_int4_outlier_channel_in_q(D, Hq, Hkv, dtype):
+    """One channel of q 2^8 times the others, K alike there for all tokens: what tells the tokens apart is what the
+    small q elements add.  A product of a code and a q element is cut at 2^-16 of the largest |q| of the row times the
+    scale, at worst (24 bits below the largest product's exponent field, which is 2^-14 for any code of 2^-20 units):
+    D such cuts move a score by at most D 2^-16 max|q| max s scale, on top of the bounds for q without outliers."""
+    wl = make_custom(seed=13, lens=[700, 33, 1024, 5, 3000], num_q_heads=Hq, num_kv_heads=Hkv, head_dim=D,
+                     block_size=16, dtype=dtype)
+    wl.q[..., 5] = 2.0 ** 8
+    wl.k_cache0[..., 5] = 1.0
+    wl.k_new[..., 5] = 1.0
+    host, cache, bt, lens = _pool_step(wl)
+    rows, out, lse, bound, lse_bound = reference(wl.q, *host, bt, lens, wl.scale)
+    d2 = D * 2.0 ** -16 * wl.q.float().abs().max().item() * float(np.abs(host[2][..., 0]).max()) * wl.scale
+    most = (np.abs(host[3][..., 0]) * (15 + np.abs(host[3][..., 1]))).max()  # of any |v|
+    _check_decode(wl, cache, bt, lens, (rows, out, lse, bound + 2 * d2 * 2 * most, lse_bound + d2), "int4 outlier in q")
+
+
 @pytest.mark.parametrize("order", ["rising", "falling", "mixed"])
 def test_decode_int4_logits_and_scales_moving_along_a_sequence(order):
     """Keys whose logits rise (or fall) by hundreds along the sequence and value rows scaled over 2^+-30: the
