@@ -359,8 +359,9 @@ int pa_decode_int8(const void* q, const void* k_codes, const void* v_codes, cons
 /* (what later reads see, for the attention of the same step); they may be  */
 /* k and v themselves.  Rows of a token without a slot are left alone       */
 /* everywhere; a slot >= num_blocks * block_size writes nothing and sets    */
-/* PA_ERRBIT_INDEX.  num_tokens * Hkv * D / 8 must be below 2^31            */
-/* (PA_ERR_UNSUPPORTED otherwise).  Launch rules of pa_write_kv.            */
+/* PA_ERRBIT_INDEX; duplicate slots are undefined.  num_tokens * Hkv * D / 8*/
+/* must be below 2^31 (PA_ERR_UNSUPPORTED otherwise).  Launch rules of      */
+/* pa_write_kv.                                                             */
 /* ------------------------------------------------------------------------ */
 int pa_write_kv_int4(const void* k, const void* v, const int64_t* slot_mapping, int num_tokens, void* k_codes,
                      void* v_codes, void* k_params, void* v_params, void* k_out, void* v_out, int num_blocks,
@@ -383,7 +384,7 @@ int pa_rope_write_kv_int4(const void* q, void* q_out, const void* k, const void*
 /* the codes and parameters becomes a bitwise copy of block pairs[2i].  A   */
 /* source may repeat; destinations must be distinct from one another and    */
 /* from every source.  An id out of range skips its pair and sets           */
-/* PA_ERRBIT_INDEX.                                                         */
+/* PA_ERRBIT_INDEX.  Launch rules of pa_write_kv, as for all INT4 calls.    */
 int pa_copy_blocks_int4(const int32_t* pairs, int num_pairs, void* k_codes, void* v_codes, void* k_params,
                         void* v_params, int num_blocks, int block_size, int num_kv_heads, int head_dim, void* stream);
 
@@ -414,7 +415,10 @@ int pa_load_blocks_int4(const int32_t* pairs, int num_pairs, const void* k_codes
 /* the V product times the V scale, as fp16.  The matrix unit cuts what a   */
 /* q element adds to a score at about 2^-18 of the largest q of the 16 it   */
 /* adds up at once, per unit of a code: q elements 2^7 times smaller than   */
-/* that still count to 11 bits, those 2^18 times smaller not at all.        */
+/* that still count to 11 bits, those 2^18 times smaller not at all; below  */
+/* 2^-28 of the largest finite q of its KV head's group an element loses    */
+/* bits of its own.  An infinity or NaN in q spoils its own head.           */
+/* Parameters not written by these calls: s >= 0, |z| < 65504.              */
 int pa_decode_int4_plan(int batch, int num_q_heads, int num_kv_heads, int head_dim, int max_context_len,
                         int num_partitions_or_0, int* grid_out, int* max_pieces_out, size_t* workspace_bytes_out);
 size_t pa_decode_int4_workspace_size(int batch, int num_q_heads, int num_kv_heads, int head_dim,

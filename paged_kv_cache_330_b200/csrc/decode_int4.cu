@@ -274,7 +274,23 @@ struct State {
         }
       }
     const float2 top2 = Elt<DT>::to_f2(top);
-    const float amax = warp_max(fmaxf(top2.x, top2.y));
+    float amax = warp_max(fmaxf(top2.x, top2.y));
+    if (amax == INFINITY) {  // a head of the group is lost; the scale of the others is that of the finite values
+      float finite = 0.f;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < WPL; ++i) {
+          const uint32_t w[4] = {raw[nt][i].x, raw[nt][i].y, raw[nt][i].z, raw[nt][i].w};
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const float2 v = Elt<DT>::to_f2(w[m]);
+            if (fabsf(v.x) < INFINITY) finite = fmaxf(finite, fabsf(v.x));
+            if (fabsf(v.y) < INFINITY) finite = fmaxf(finite, fabsf(v.y));
+          }
+        }
+      amax = warp_max(finite);
+    }
     int e = 0;
     if (amax > 0.f) {
       int k;

@@ -340,6 +340,21 @@ def test_decode_int4_outlier_channel_in_q(D, Hq, Hkv, dtype):
     _check_decode(wl, cache, bt, lens, (rows, out, lse, bound + 2 * d2 * 2 * most, lse_bound + d2), "int4 outlier in q")
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,dtype", [(8, 2, 128, "bf16"), (8, 1, 64, "f16"), (16, 1, 128, "bf16")])
+def test_decode_int4_not_finite_q_spoils_its_own_head(Hq, Hkv, D, dtype):
+    wl = make_custom(seed=14, lens=[70, 1, 2000, 33], num_q_heads=Hq, num_kv_heads=Hkv, head_dim=D, block_size=16,
+                     dtype=dtype)
+    host, cache, bt, lens = _pool_step(wl)
+    rows, out, lse, bound, lse_bound = reference(wl.q, *host, bt, lens, wl.scale)
+    q = wl.q.clone()
+    q[0, 1, 7], q[1, 0, 0], q[2, 3, D - 1], q[2, 2, 1] = float("inf"), float("nan"), float("-inf"), float("nan")
+    lost = {(0, 1), (1, 0), (2, 3), (2, 2)}
+    wl.q = q
+    keep = [i for i, r in enumerate(rows) if tuple(r) not in lost]
+    _check_decode(wl, cache, bt, lens, ([rows[i] for i in keep], out[keep], lse[keep], bound[keep], lse_bound[keep]),
+                  "int4 inf and nan in q")
+
+
 @pytest.mark.parametrize("order", ["rising", "falling", "mixed"])
 def test_decode_int4_logits_and_scales_moving_along_a_sequence(order):
     """Keys whose logits rise (or fall) by hundreds along the sequence and value rows scaled over 2^+-30: the
