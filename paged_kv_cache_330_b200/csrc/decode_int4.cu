@@ -20,7 +20,8 @@
 // the line, so results do not depend on timing.
 //
 // Mathematics.  Products run on mma.m16n8k16 (fp16 in, fp32 out) with tokens (scores) or columns (PV) as the 16
-// rows and up to 8 heads of the group as the 8 columns; G 16 takes two column tiles.
+// rows and up to 8 heads of the group as the 8 columns.  A group of 16 is two halves: CTAs 2i and 2i + 1 walk the same
+// part of the line, each for 8 heads; what the second one reads comes from L2.
 //   * Codes enter as fp16 subnormals: a nibble in the low four bits of a half is code * 2^-24, in the next four
 //     code * 2^-20, exactly, with no offset to take out again.  Widening a word of 8 codes of V is one shift and four
 //     ANDs; the factors 2^24 and 16 sit in the final scaling of the output rows.  The matrix unit lines products up by
@@ -233,62 +234,56 @@ constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;  // a nibble of each
 // ------------------------------------------------------------------ a warp's state over one piece
 template <int DT, int D, int G>
 struct State {
-  static constexpr int NG = D / 64, KS = D / 16, NT = (G + 7) / 8, WPL = D / 32;  // WPL: K words a lane reads of a row
-  uint32_t qb[NT][KS][2];  // q as B operand (fp16, prescaled)
-  uint32_t qsum[NT][NG];   // B operand of the zero-point product: lanes c = 0 the sum of q over a group, 2^-14 of it in two terms
-  float o[NT][KS][4];      // O^T times 2^-24 (rows g) and 2^-20 (rows g + 8), columns heads
-  float z[NT][NG][4];      // sum P' z_V (columns heads; all rows alike)
-  float l[NT][2];          // this lane's part of sum 2^(x - R)
-  float R[NT][2];
-  float qs;                // scale * log2(e) * 2^20 / prescale
-  bool fresh;              // some head has met no non-zero V scale yet: its R is not set
+  static constexpr int NG = D / 64, KS = D / 16, WPL = D / 32;  // WPL: K words a lane reads of a row
+  uint32_t qb[KS][2];  // q as B operand (fp16, prescaled)
+  uint32_t qsum[NG];   // B operand of the zero-point product: lanes c = 0 the sum of q over a group, 2^-14 of it in two terms
+  float o[KS][4];      // O^T times 2^-24 (rows g) and 2^-20 (rows g + 8), columns heads
+  float z[NG][4];      // sum P' z_V (columns heads; all rows alike)
+  float l[2];          // this lane's part of sum 2^(x - R)
+  float R[2];
+  float qs;            // scale * log2(e) * 2^20 / prescale
+  bool fresh;          // some head has met no non-zero V scale yet: its R is not set
 
   // qrows: the group's [G][D] rows of q.  A lane loads just the values its operands hold.
   template <bool in_shared>
   __device__ __forceinline__ void begin(const uint8_t* qrows, float scale_log2, int lane) {
     const int g = lane >> 2, c = lane & 3;
-    uint4 raw[NT][WPL];
+    uint4 raw[WPL];
     using T2 = typename Elt<DT>::T2;
     uint32_t top = 0;  // largest magnitudes, two columns at once
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int i = 0; i < WPL; ++i) {
-        // stored word WPL * c + i of a row: 8 values from `base` on
-        const int base = D == 128 ? 64 * (i & 1) + 8 * (2 * c + (i >> 1)) : 8 * (2 * c + i);
-        raw[nt][i] = make_uint4(0, 0, 0, 0);
-        if (nt * 8 + g < G) {
-          const uint4* at = reinterpret_cast<const uint4*>(qrows + ((nt * 8 + g) * D + base) * 2);
-          raw[nt][i] = in_shared ? *at : __ldcg(at);
-        }
+    for (int i = 0; i < WPL; ++i) {
+      // stored word WPL * c + i of a row: 8 values from `base` on
+      const int base = D == 128 ? 64 * (i & 1) + 8 * (2 * c + (i >> 1)) : 8 * (2 * c + i);
+      raw[i] = make_uint4(0, 0, 0, 0);
+      if (g < G) {
+        const uint4* at = reinterpret_cast<const uint4*>(qrows + (g * D + base) * 2);
+        raw[i] = in_shared ? *at : __ldcg(at);
       }
+    }
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int i = 0; i < WPL; ++i) {
+      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
-      for (int i = 0; i < WPL; ++i) {
-        const uint32_t w[4] = {raw[nt][i].x, raw[nt][i].y, raw[nt][i].z, raw[nt][i].w};
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          const T2 v = __hmax2(*reinterpret_cast<T2*>(&top), __habs2(*reinterpret_cast<const T2*>(&w[m])));
-          top = *reinterpret_cast<const uint32_t*>(&v);
-        }
+      for (int m = 0; m < 4; ++m) {
+        const T2 v = __hmax2(*reinterpret_cast<T2*>(&top), __habs2(*reinterpret_cast<const T2*>(&w[m])));
+        top = *reinterpret_cast<const uint32_t*>(&v);
       }
+    }
     const float2 top2 = Elt<DT>::to_f2(top);
     float amax = warp_max(fmaxf(top2.x, top2.y));
     if (amax == INFINITY) {  // a head of the group is lost; the scale of the others is that of the finite values
       float finite = 0.f;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int i = 0; i < WPL; ++i) {
+        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
-        for (int i = 0; i < WPL; ++i) {
-          const uint32_t w[4] = {raw[nt][i].x, raw[nt][i].y, raw[nt][i].z, raw[nt][i].w};
-#pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            const float2 v = Elt<DT>::to_f2(w[m]);
-            if (fabsf(v.x) < INFINITY) finite = fmaxf(finite, fabsf(v.x));
-            if (fabsf(v.y) < INFINITY) finite = fmaxf(finite, fabsf(v.y));
-          }
+        for (int m = 0; m < 4; ++m) {
+          const float2 v = Elt<DT>::to_f2(w[m]);
+          if (fabsf(v.x) < INFINITY) finite = fmaxf(finite, fabsf(v.x));
+          if (fabsf(v.y) < INFINITY) finite = fmaxf(finite, fabsf(v.y));
         }
+      }
       amax = warp_max(finite);
     }
     int e = 0;
@@ -300,87 +295,82 @@ struct State {
     const float f = __int_as_float((127 + e) << 23), finv = __int_as_float((127 - e) << 23);
     qs = scale_log2 * finv * kUnitK;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int i = 0; i < WPL; ++i) {
+      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+      float x[8];
 #pragma unroll
-      for (int i = 0; i < WPL; ++i) {
-        const uint32_t w[4] = {raw[nt][i].x, raw[nt][i].y, raw[nt][i].z, raw[nt][i].w};
-        float x[8];
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          const float2 v = Elt<DT>::to_f2(w[m]);
-          x[2 * m] = v.x * f;
-          x[2 * m + 1] = v.y * f;
-        }
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          qb[nt][2 * i + s][0] = pack_h2(x[2 * s], x[2 * s + 4]);
-          qb[nt][2 * i + s][1] = pack_h2(x[2 * s + 1], x[2 * s + 5]);
-        }
+      for (int m = 0; m < 4; ++m) {
+        const float2 v = Elt<DT>::to_f2(w[m]);
+        x[2 * m] = v.x * f;
+        x[2 * m + 1] = v.y * f;
       }
 #pragma unroll
-      for (int grp = 0; grp < NG; ++grp) {
-        float acc[4];
-#pragma unroll
-        for (int i = grp; i < WPL; i += NG)
-#pragma unroll
-          for (int s = 0; s < 2; ++s)
-            mma_f16(i == grp && s == 0, acc, kOnes, kOnes, kOnes, kOnes, qb[nt][2 * i + s][0], qb[nt][2 * i + s][1]);
-        // lane g takes head 8nt + g, which column 2 (g / 2) + g % 2 of any row holds
-        const float s0 = __shfl_sync(0xffffffffu, acc[0], g >> 1), s1 = __shfl_sync(0xffffffffu, acc[1], g >> 1);
-        const float sum = ((g & 1) ? s1 : s0) * (64.f / kUnitK), hi = __half2float(__float2half_rn(sum));
-        qsum[nt][grp] = c == 0 ? pack_h2(hi, sum - hi) : 0u;
-        z[nt][grp][0] = z[nt][grp][1] = z[nt][grp][2] = z[nt][grp][3] = 0.f;
+      for (int s = 0; s < 2; ++s) {
+        qb[2 * i + s][0] = pack_h2(x[2 * s], x[2 * s + 4]);
+        qb[2 * i + s][1] = pack_h2(x[2 * s + 1], x[2 * s + 5]);
       }
-#pragma unroll
-      for (int i = 0; i < KS; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
-      l[nt][0] = l[nt][1] = 0.f;
-      R[nt][0] = R[nt][1] = kGuess;
     }
+#pragma unroll
+    for (int grp = 0; grp < NG; ++grp) {
+      float acc[4];
+#pragma unroll
+      for (int i = grp; i < WPL; i += NG)
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+          mma_f16(i == grp && s == 0, acc, kOnes, kOnes, kOnes, kOnes, qb[2 * i + s][0], qb[2 * i + s][1]);
+      // lane g takes head g, which column 2 (g / 2) + g % 2 of any row holds
+      const float s0 = __shfl_sync(0xffffffffu, acc[0], g >> 1), s1 = __shfl_sync(0xffffffffu, acc[1], g >> 1);
+      const float sum = ((g & 1) ? s1 : s0) * (64.f / kUnitK), hi = __half2float(__float2half_rn(sum));
+      qsum[grp] = c == 0 ? pack_h2(hi, sum - hi) : 0u;
+      z[grp][0] = z[grp][1] = z[grp][2] = z[grp][3] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < KS; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    l[0] = l[1] = 0.f;
+    R[0] = R[1] = kGuess;
     fresh = true;
   }
 
   // Moves the references of the heads that need it, so that the tile's scores x (relative to R; -inf where
   // masked) give P' <= 2^4 and l <= 2^91.  svm: the larger V scale of each of this lane's rows.
-  __device__ __forceinline__ void rebase(float (&x)[2][NT][4], const float (&svm)[4]) {
+  __device__ __forceinline__ void rebase(float (&x)[2][4], const float (&svm)[4]) {
     bool still = false;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int e = 0; e < 2; ++e) {
+      float u = -INFINITY, v = l[e] > 0.f ? __log2f(l[e]) : -INFINITY;
+      bool set = false;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float u = -INFINITY, v = l[nt][e] > 0.f ? __log2f(l[nt][e]) : -INFINITY;
-        bool set = false;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float xr = x[r >> 1][nt][2 * (r & 1) + e];
-          v = fmaxf(v, xr);
-          u = fmaxf(u, svm[r] > 0.f ? xr + __log2f(svm[r]) : -INFINITY);
-        }
-#pragma unroll
-        for (int i = 0; i < KS; ++i) set |= o[nt][i][e] != 0.f || o[nt][i][2 + e] != 0.f;
-#pragma unroll
-        for (int grp = 0; grp < NG; ++grp) set |= z[nt][grp][e] != 0.f;
-        // every lane of a column has to agree on whether its O is still all zero
-        float any = set ? 1.f : 0.f;
-        u = rows_max(u);
-        v = rows_max(v);
-        set = rows_max(any) > 0.f;
-        float up = fmaxf(u - 4.f, v - 90.f);
-        if (set) up = fmaxf(up, 0.f);
-        else if (u == -INFINITY) up = v, still = true;
-        up = ceilf(up);
-        if (!(fabsf(up) < 1e30f)) up = 0.f;  // not-a-number inputs: leave the references alone
-        const float f = exp2f(-up);
-        if (l[nt][e] > 0.f) l[nt][e] *= f;
-        if (set) {
-#pragma unroll
-          for (int i = 0; i < KS; ++i) o[nt][i][e] *= f, o[nt][i][2 + e] *= f;
-#pragma unroll
-          for (int grp = 0; grp < NG; ++grp) z[nt][grp][e] *= f, z[nt][grp][2 + e] *= f;
-        }
-        R[nt][e] += up;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) x[r >> 1][nt][2 * (r & 1) + e] -= up;
+      for (int r = 0; r < 4; ++r) {
+        const float xr = x[r >> 1][2 * (r & 1) + e];
+        v = fmaxf(v, xr);
+        u = fmaxf(u, svm[r] > 0.f ? xr + __log2f(svm[r]) : -INFINITY);
       }
+#pragma unroll
+      for (int i = 0; i < KS; ++i) set |= o[i][e] != 0.f || o[i][2 + e] != 0.f;
+#pragma unroll
+      for (int grp = 0; grp < NG; ++grp) set |= z[grp][e] != 0.f;
+      // every lane of a column has to agree on whether its O is still all zero
+      float any = set ? 1.f : 0.f;
+      u = rows_max(u);
+      v = rows_max(v);
+      set = rows_max(any) > 0.f;
+      float up = fmaxf(u - 4.f, v - 90.f);
+      if (set) up = fmaxf(up, 0.f);
+      else if (u == -INFINITY) up = v, still = true;
+      up = ceilf(up);
+      if (!(fabsf(up) < 1e30f)) up = 0.f;  // not-a-number inputs: leave the references alone
+      const float f = exp2f(-up);
+      if (l[e] > 0.f) l[e] *= f;
+      if (set) {
+#pragma unroll
+        for (int i = 0; i < KS; ++i) o[i][e] *= f, o[i][2 + e] *= f;
+#pragma unroll
+        for (int grp = 0; grp < NG; ++grp) z[grp][e] *= f, z[grp][2 + e] *= f;
+      }
+      R[e] += up;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) x[r >> 1][2 * (r & 1) + e] -= up;
+    }
     fresh = __any_sync(0xffffffffu, still);
   }
 
@@ -442,8 +432,8 @@ struct State {
     // the tile's largest V scale (not negative: its bits order as its value does)
     const float sv_top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(NG == 2 ? fmaxf(vs[0], vs[NG - 1]) : vs[0])));
     __syncwarp();
-    // ---- scores relative to R, columns heads 8nt + 2c + {0,1}
-    float x[2][NT][4];
+    // ---- scores relative to R, columns heads 2c + {0,1}
+    float x[2][4];
     uint32_t times16;  // a shift by 4 on the multiplier's pipe: the compiler, seeing the 16, would shift twice on the other
     asm("mov.u32 %0, 16;" : "=r"(times16));
 #pragma unroll
@@ -463,33 +453,27 @@ struct State {
           kz[hh][0] = u.y;
         }
       }
-      float acc[NT][NG][4];
+      float acc[NG][4];
 #pragma unroll
       for (int i = 0; i < WPL; ++i)
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           const uint32_t a = kc[2 * mt][i] >> (8 * s), b = kc[2 * mt + 1][i] >> (8 * s);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma_f16(i < NG && s == 0, acc[nt][i % NG], a * times16 & kHigh, b * times16 & kHigh, a & kHigh, b & kHigh,
-                    qb[nt][2 * i + s][0], qb[nt][2 * i + s][1]);
+          mma_f16(i < NG && s == 0, acc[i % NG], a * times16 & kHigh, b * times16 & kHigh, a & kHigh, b & kHigh,
+                  qb[2 * i + s][0], qb[2 * i + s][1]);
         }
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int grp = 0; grp < NG; ++grp) {
+        mma_f16(acc[grp], kz[0][grp], kz[1][grp], kz[0][grp], kz[1][grp], qsum[grp], 0u);
 #pragma unroll
-        for (int grp = 0; grp < NG; ++grp) {
-          mma_f16(acc[nt][grp], kz[0][grp], kz[1][grp], kz[0][grp], kz[1][grp], qsum[nt][grp], 0u);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            x[mt][nt][e] = fmaf(acc[nt][grp][e], ks[e >> 1][grp], grp == 0 ? -R[nt][e & 1] : x[mt][nt][e]);
-        }
+        for (int e = 0; e < 4; ++e)
+          x[mt][e] = fmaf(acc[grp][e], ks[e >> 1][grp], grp == 0 ? -R[e & 1] : x[mt][e]);
+      }
     }
     if (nv < kTile) {
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        if (8 * r + g >= nv)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) x[r >> 1][nt][2 * (r & 1)] = x[r >> 1][nt][2 * (r & 1) + 1] = -INFINITY;
+        if (8 * r + g >= nv) x[r >> 1][2 * (r & 1)] = x[r >> 1][2 * (r & 1) + 1] = -INFINITY;
     }
     // ---- weights; taken once more after a move of the references
     float sv[4][NG];
@@ -504,43 +488,37 @@ struct State {
         sv[r][0] = a[0];
       }
     }
-    uint32_t pk[NT][NG][4];
-    float sum[NT][2];
+    uint32_t pk[NG][4];
+    float sum[2];
     for (bool moved = false;; moved = true) {
       bool move = false;
+      sum[0] = sum[1] = 0.f;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        sum[nt][0] = sum[nt][1] = 0.f;
+      for (int r = 0; r < 4; ++r) {
+        const float p0 = fast_exp2(x[r >> 1][2 * (r & 1)]), p1 = fast_exp2(x[r >> 1][2 * (r & 1) + 1]);
+        sum[0] += p0;
+        sum[1] += p1;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float p0 = fast_exp2(x[r >> 1][nt][2 * (r & 1)]), p1 = fast_exp2(x[r >> 1][nt][2 * (r & 1) + 1]);
-          sum[nt][0] += p0;
-          sum[nt][1] += p1;
+        for (int grp = 0; grp < NG; ++grp) pk[grp][r] = pack_h2(p0 * sv[r][grp], p1 * sv[r][grp]);
+      }
+      // each P' is at most the lane's sum times the largest scale: below 2^15, and l below 2^100
 #pragma unroll
-          for (int grp = 0; grp < NG; ++grp) pk[nt][grp][r] = pack_h2(p0 * sv[r][grp], p1 * sv[r][grp]);
-        }
-        // each P' is at most the lane's sum times the largest scale: below 2^15, and l below 2^100
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          move |= !(sum[nt][e] * sv_top < 32768.f);
-          sum[nt][e] += l[nt][e];
-          move |= !(sum[nt][e] < 1.2676506e30f);
-        }
+      for (int e = 0; e < 2; ++e) {
+        move |= !(sum[e] * sv_top < 32768.f);
+        sum[e] += l[e];
+        move |= !(sum[e] < 1.2676506e30f);
       }
       move = __any_sync(0xffffffffu, move);
       if (fresh && !move) {  // is the guess large enough for every head?
         bool low = false;
+        __half2 top = as_h2(0u);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          __half2 top = as_h2(0u);
+        for (int grp = 0; grp < NG; ++grp)
 #pragma unroll
-          for (int grp = 0; grp < NG; ++grp)
+          for (int r = 0; r < 4; ++r) top = __hmax2(top, as_h2(pk[grp][r]));
 #pragma unroll
-            for (int r = 0; r < 4; ++r) top = __hmax2(top, as_h2(pk[nt][grp][r]));
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) top = __hmax2(top, as_h2(__shfl_xor_sync(0xffffffffu, as_u32(top), o)));
-          low |= !(__low2float(top) >= 8.f) || !(__high2float(top) >= 8.f);
-        }
+        for (int o = 4; o < 32; o <<= 1) top = __hmax2(top, as_h2(__shfl_xor_sync(0xffffffffu, as_u32(top), o)));
+        low |= !(__low2float(top) >= 8.f) || !(__high2float(top) >= 8.f);
         move = __any_sync(0xffffffffu, low);
         fresh = move;
       }
@@ -550,15 +528,12 @@ struct State {
       for (int r = 0; r < 4; ++r) svm[r] = NG == 2 ? fmaxf(sv[r][0], sv[r][NG - 1]) : sv[r][0];
       rebase(x, svm);
     }
+    l[0] = sum[0];
+    l[1] = sum[1];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      l[nt][0] = sum[nt][0];
-      l[nt][1] = sum[nt][1];
+    for (int grp = 0; grp < NG; ++grp)
 #pragma unroll
-      for (int grp = 0; grp < NG; ++grp)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) pk[nt][grp][r] = trans8x8(pk[nt][grp][r]);  // tokens along the rows of the B operand
-    }
+      for (int r = 0; r < 4; ++r) pk[grp][r] = trans8x8(pk[grp][r]);  // tokens along the rows of the B operand
     // ---- O^T += V^T P'^T: tokens 2c, 2c + 1, 2c + 8, 2c + 9 of each half; word `grp` of lane g's piece of a row holds
     // values 64 grp + 8 g ..
     // (codes lie swizzled, see bring; odd c take their two tokens in the other order, which with the swizzle spreads
@@ -590,10 +565,8 @@ struct State {
         for (int grp = 0; grp < NG; ++grp) zp[hh][grp] = a[grp];
       }
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int grp = 0; grp < NG; ++grp)
-          mma_f16(z[nt][grp], zp[0][grp], zp[0][grp], zp[1][grp], zp[1][grp], pk[nt][grp][2 * mt], pk[nt][grp][2 * mt + 1]);
+      for (int grp = 0; grp < NG; ++grp)
+        mma_f16(z[grp], zp[0][grp], zp[0][grp], zp[1][grp], zp[1][grp], pk[grp][2 * mt], pk[grp][2 * mt + 1]);
 #pragma unroll
       for (int grp = 0; grp < NG; ++grp)
 #pragma unroll
@@ -603,10 +576,8 @@ struct State {
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
             const uint32_t as = a >> (8 * s), bs = b >> (8 * s);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma_f16(o[nt][4 * grp + 2 * half + s], as & kLow, as & kHigh, bs & kLow, bs & kHigh,
-                      pk[nt][grp][2 * mt], pk[nt][grp][2 * mt + 1]);
+            mma_f16(o[4 * grp + 2 * half + s], as & kLow, as & kHigh, bs & kLow, bs & kHigh,
+                    pk[grp][2 * mt], pk[grp][2 * mt + 1]);
           }
         }
     }
@@ -615,29 +586,29 @@ struct State {
   // Completes the lanes' parts of l.
   __device__ __forceinline__ void finish() {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) l[nt][e] = rows_sum(l[nt][e]);
+    for (int e = 0; e < 2; ++e) l[e] = rows_sum(l[e]);
   }
-  // The 8 output values 64 grp + 8 g .. of head 8nt + 2c + e, relative to R.
-  __device__ __forceinline__ void values(int nt, int grp, int e, float (&v)[8]) const {
+  // The 8 output values 64 grp + 8 g .. of head 2c + e, relative to R.
+  __device__ __forceinline__ void values(int grp, int e, float (&v)[8]) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      v[2 * i] = fmaf(o[nt][4 * grp + i][e], kUnit, z[nt][grp][e]);
-      v[2 * i + 1] = fmaf(o[nt][4 * grp + i][2 + e], kUnit / 16.f, z[nt][grp][e]);
+      v[2 * i] = fmaf(o[4 * grp + i][e], kUnit, z[grp][e]);
+      v[2 * i + 1] = fmaf(o[4 * grp + i][2 + e], kUnit / 16.f, z[grp][e]);
     }
   }
 };
 
 // ------------------------------------------------------------------ kernel
-template <int DT, int D, int G, int NW, int NS>
+template <int DT, int D, int G, int HV, int NW, int NS>
 __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p) {
   using LY = Layout<D, G, NW, NS>;
   using S = State<DT, D, G>;
   using T = typename Elt<DT>::T;
   static_assert(NW <= 16, "a warp's lanes hold all pieces of the CTA");
   extern __shared__ __align__(128) uint8_t smem[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // HV CTAs walk the same part of the line, each for G heads of a group of HV * G
+  const int half = HV == 2 ? blockIdx.x & 1 : 0, cta = blockIdx.x / HV, line_ctas = gridDim.x / HV;
   long long* warp_tiles = reinterpret_cast<long long*>(smem + LY::SCAN_OFF);
   int* warp_longest = reinterpret_cast<int*>(smem + LY::LONG_OFF);
   long long* incl_s = reinterpret_cast<long long*>(smem + LY::INCL_OFF);
@@ -649,7 +620,7 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
   // The block tables come from HBM on their first use: ask for them (a line a thread, at most) while the lengths are
   // added up.
   {
-    const size_t line = (size_t)cta * (NW * 32) + threadIdx.x, bytes = (size_t)B * p.max_blocks_per_seq * 4;
+    const size_t line = (size_t)blockIdx.x * (NW * 32) + threadIdx.x, bytes = (size_t)B * p.max_blocks_per_seq * 4;
     if (line * 128 < bytes)
       asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const uint8_t*>(p.block_tables) + line * 128));
   }
@@ -671,7 +642,7 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
       incl += places_of(Lc);
       longest = max(longest, tiles_of(Lc));
     }
-    if (clamped && cta == 0) PA_RECORD_ERROR(PA_ERRBIT_INDEX);
+    if (clamped && blockIdx.x == 0) PA_RECORD_ERROR(PA_ERRBIT_INDEX);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long t = __shfl_up_sync(0xffffffffu, incl, o);
@@ -692,7 +663,7 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
     if (lane >= o) wincl += t;
   }
   const long long total = __shfl_sync(0xffffffffu, wincl, NW - 1) * Hkv;
-  const long long ctas = min((long long)gridDim.x, total);
+  const long long ctas = min((long long)line_ctas, total);
   const bool narrow = (total + 1) * (ctas + 1) < (1ll << 32);
   // The segment at place x of the line, and the tile (the segment's first one, if x is one of its kStart places).
   auto find = [&](long long x) {
@@ -779,8 +750,9 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
     }
     ++filed;
   };
+  auto head0 = [&](size_t seg) { return (seg * HV + half) * G; };  // of a segment: the first row of q, out and lse
   auto q_rows = [&](int b, int kvh) {
-    return reinterpret_cast<const uint8_t*>(p.q) + ((size_t)b * p.num_q_heads + (size_t)kvh * G) * D * 2;
+    return reinterpret_cast<const uint8_t*>(p.q) + head0((size_t)b * p.num_kv_heads + kvh) * D * 2;
   };
   auto bring_q = [&](const Walk& w) {  // of the piece filed last, with its first tile
     if constexpr (LY::QS) {
@@ -858,7 +830,7 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
     cp_async_commit();
   }
   // sequences without a token: zeros, and a log-sum-exp of -inf
-  for (int i = cta * NW + warp; i < B; i += gridDim.x * NW) {
+  for (int i = blockIdx.x * NW + warp; i < B; i += gridDim.x * NW) {
     if (len_of(i) != 0) continue;
     uint4* o4 = reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.out) + (size_t)i * p.num_q_heads * D);
     for (int e = lane; e < p.num_q_heads * D / 8; e += 32) o4[e] = make_uint4(0, 0, 0, 0);
@@ -901,51 +873,47 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
     const bool head = de.w == 0, tail = rem <= 0;
     const int g = lane >> 2, c = lane & 3;
     if (head && tail) {
-      T* out = reinterpret_cast<T*>(p.out) + ((size_t)b * p.num_q_heads + (size_t)kvh * G) * D;
+      const size_t row0 = head0((size_t)b * p.num_kv_heads + kvh);
+      T* out = reinterpret_cast<T*>(p.out) + row0 * D;
 #pragma unroll
-      for (int n = 0; n < S::NT; ++n)
+      for (int e = 0; e < 2; ++e) {
+        const int h = 2 * c + e;
+        if (h >= G) continue;
+        const float inv = 1.f / st.l[e];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int h = 8 * n + 2 * c + e;
-          if (h >= G) continue;
-          const float inv = 1.f / st.l[n][e];
-#pragma unroll
-          for (int grp = 0; grp < S::NG; ++grp) {
-            float v[8];
-            st.values(n, grp, e, v);
-            uint4 u;
-            u.x = Elt<DT>::from_f2(v[0] * inv, v[1] * inv);
-            u.y = Elt<DT>::from_f2(v[2] * inv, v[3] * inv);
-            u.z = Elt<DT>::from_f2(v[4] * inv, v[5] * inv);
-            u.w = Elt<DT>::from_f2(v[6] * inv, v[7] * inv);
-            st_v4(out + h * D + 64 * grp + 8 * g, u);
-          }
-          if (p.lse && g == 0)
-            p.lse[(size_t)b * p.num_q_heads + (size_t)kvh * G + h] = (st.R[n][e] + __log2f(st.l[n][e])) * kLn2;
+        for (int grp = 0; grp < S::NG; ++grp) {
+          float v[8];
+          st.values(grp, e, v);
+          uint4 u;
+          u.x = Elt<DT>::from_f2(v[0] * inv, v[1] * inv);
+          u.y = Elt<DT>::from_f2(v[2] * inv, v[3] * inv);
+          u.z = Elt<DT>::from_f2(v[4] * inv, v[5] * inv);
+          u.w = Elt<DT>::from_f2(v[6] * inv, v[7] * inv);
+          st_v4(out + h * D + 64 * grp + 8 * g, u);
         }
+        if (p.lse && g == 0) p.lse[row0 + h] = (st.R[e] + __log2f(st.l[e])) * kLn2;
+      }
     } else {
       const int which = piece + 1 == filed;  // the warp's last piece lies in its ring, which is done with
       float* part = reinterpret_cast<float*>(which ? smem + LY::RING_OFF + warp * LY::RING
                                                    : smem + LY::PART_OFF + warp * LY::PART);
 #pragma unroll
-      for (int n = 0; n < S::NT; ++n)
+      for (int e = 0; e < 2; ++e) {
+        const int h = 2 * c + e;
+        if (h >= G) continue;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int h = 8 * n + 2 * c + e;
-          if (h >= G) continue;
-#pragma unroll
-          for (int grp = 0; grp < S::NG; ++grp) {
-            float v[8];
-            st.values(n, grp, e, v);
-            float4* o4 = reinterpret_cast<float4*>(part + h * D + 64 * grp + 8 * g);
-            o4[0] = make_float4(v[0], v[1], v[2], v[3]);
-            o4[1] = make_float4(v[4], v[5], v[6], v[7]);
-          }
-          if (g == 0) {
-            part[G * D + h] = st.R[n][e];
-            part[G * D + G + h] = st.l[n][e];
-          }
+        for (int grp = 0; grp < S::NG; ++grp) {
+          float v[8];
+          st.values(grp, e, v);
+          float4* o4 = reinterpret_cast<float4*>(part + h * D + 64 * grp + 8 * g);
+          o4[0] = make_float4(v[0], v[1], v[2], v[3]);
+          o4[1] = make_float4(v[4], v[5], v[6], v[7]);
         }
+        if (g == 0) {
+          part[G * D + h] = st.R[e];
+          part[G * D + G + h] = st.l[e];
+        }
+      }
       if (lane == 0) {
         Piece pc;
         pc.b = b;
@@ -1031,6 +999,9 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
   // columns: a thread takes 4 of a head.  Cut segments first: this CTA's shares of them go to the workspace, slot
   // segment + CTA (a CTA holds at most one share of a segment, and neighbouring segments share at most one CTA).
   constexpr int QUADS = G * D / 4;
+  const size_t ws_row0 = (size_t)half * (B * (size_t)Hkv + line_ctas) * G;  // each half has slots and counters of its own
+  float *ws_r = p.ws_r + ws_row0, *ws_l = p.ws_l + ws_row0, *ws_o = p.ws_o + ws_row0 * D;
+  int* ws_cnt = p.ws_cnt + half * (kMaxGrid / 2);
   auto columns = [&](int from, int to) {
     for (int q = from * QUADS + threadIdx.x; q < to * QUADS; q += NW * 32) {
       const int k = q / QUADS, e = q - k * QUADS, h = e / (D / 4), col = e % (D / 4) * 4;
@@ -1051,14 +1022,14 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
         uint2 u;
         u.x = Elt<DT>::from_f2(acc.x * inv, acc.y * inv);
         u.y = Elt<DT>::from_f2(acc.z * inv, acc.w * inv);
-        *reinterpret_cast<uint2*>(reinterpret_cast<T*>(p.out) + (seg * G + h) * D + col) = u;
-        if (p.lse && col == 0) p.lse[seg * G + h] = (md.x + __log2f(md.y)) * kLn2;
+        *reinterpret_cast<uint2*>(reinterpret_cast<T*>(p.out) + (head0(seg) + h) * D + col) = u;
+        if (p.lse && col == 0) p.lse[head0(seg) + h] = (md.x + __log2f(md.y)) * kLn2;
       } else {
         const size_t row = (seg + cta) * G + h;
-        *reinterpret_cast<float4*>(p.ws_o + row * D + col) = acc;
+        *reinterpret_cast<float4*>(ws_o + row * D + col) = acc;
         if (col == 0) {
-          p.ws_r[row] = md.x;
-          p.ws_l[row] = md.y;
+          ws_r[row] = md.x;
+          ws_l[row] = md.y;
         }
       }
     }
@@ -1078,7 +1049,7 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
   // 100 GB/s.
   const int gf = max(c0, cta / kGroup * kGroup);
   const bool grouped = n_sh > 2 * kGroup;
-  int* cnt = p.ws_cnt + (grouped ? group_counter_of(c0, gf) : counter_of(c0));
+  int* cnt = ws_cnt + (grouped ? group_counter_of(c0, gf) : counter_of(c0));
   int n = grouped ? min(c0 + n_sh, (cta / kGroup + 1) * kGroup) - gf : n_sh;  // shares to join now, from slot0 on
   size_t slot0 = seg + (grouped ? gf : c0), slots = slot0;
   int step = 1;
@@ -1116,9 +1087,9 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
           for (int u = 0; u < U; ++u) {
             const int i = min(i0 + u, n_ - 1);  // share i is in slot0 for i = 0, in slots + i * step for the others
             const size_t row = (i == 0 ? slot0_ : slots_ + (size_t)i * step_) * G + h;
-            r[u] = __ldcg(p.ws_r + row);
-            l[u] = i0 + u < n_ ? __ldcg(p.ws_l + row) : 0.f;
-            v[u] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + row * D + col));
+            r[u] = __ldcg(ws_r + row);
+            l[u] = i0 + u < n_ ? __ldcg(ws_l + row) : 0.f;
+            v[u] = __ldcg(reinterpret_cast<const float4*>(ws_o + row * D + col));
           }
           float top = M[ps];
 #pragma unroll
@@ -1144,13 +1115,13 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
         if (quad >= QUADS) break;
         if (partial) {
           const size_t row = slot0_ * G + h;
-          *reinterpret_cast<float4*>(p.ws_o + row * D + col) = acc[ps];
+          *reinterpret_cast<float4*>(ws_o + row * D + col) = acc[ps];
           if (col == 0) {
-            p.ws_r[row] = M[ps];
-            p.ws_l[row] = den[ps];
+            ws_r[row] = M[ps];
+            ws_l[row] = den[ps];
           }
         } else {
-          const size_t at = seg_ * G + h;  // batch * Hq + head
+          const size_t at = head0(seg_) + h;
           const float inv = 1.f / den[ps];
           uint2 u;
           u.x = Elt<DT>::from_f2(acc[ps].x * inv, acc[ps].y * inv);
@@ -1166,7 +1137,7 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
       step = kGroup;
       n = (c0 + n_sh - 1) / kGroup - c0 / kGroup + 1;
       __syncthreads();
-      if (warp == 0 && lane == which) done_s[lane] = count_last(p.ws_cnt + counter_of(c0), n);
+      if (warp == 0 && lane == which) done_s[lane] = count_last(ws_cnt + counter_of(c0), n);
     }
   }
 }
@@ -1175,12 +1146,15 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
 // Warps of a CTA (one CTA fills an SM) and stages of each warp's ring.  D 128, G <= 8: 12 warps of 168 registers; 16 warps
 // of 128 need 590 instructions a tile instead of 522 (values kept and fetched again): 64 sequences of 4096 to 8192
 // tokens, 64 heads, take 92.9 us with 16, 89.5 with 12, 101 with 10, 107 with 8.  D 64 fits 16 (27.4 against 28.6 us,
-// 64 sequences of 500 to 8000).  G 16 holds two column tiles, 250 registers.  A third stage changes nothing.
+// 64 sequences of 500 to 8000).  A third stage changes nothing.
+// G 16 as one piece (two column tiles, 8 warps of 250 registers) against two halves on two CTAs: one sequence of 2000
+// tokens 14.7 and 11.3 us, of 100001 26.8 and 23.7, 16 of 8000 26.6 and 25.6, 64 of 100 to 8000 38.7 and 40.1 (D 128, 2
+// KV heads; D 64 10.3 and 9.8 to 27.7 and 29.4).  Halves, for all.
 constexpr int kWarps = 12;
 
 template <int D, int G>
 struct Shape {
-  static constexpr int NW = G == 16 ? 8 : (D == 64 ? 16 : kWarps);
+  static constexpr int NW = D == 64 ? 16 : kWarps;
   static constexpr int NS = 2;
 };
 
@@ -1193,19 +1167,20 @@ bool make_plan(int batch, int Hq, int Hkv, int D, int max_context_len, int num_p
   if (batch < 0 || Hq <= 0 || Hkv <= 0 || num_partitions < 0 || max_context_len < 0 || Hq % Hkv) return false;
   if (!valid_head_dim(D) || !valid_group(Hq / Hkv)) return false;
   if ((int64_t)batch * Hq >= (1ll << 31)) return false;
-  const int G = Hq / Hkv;
+  const int G = Hq / Hkv, HV = G == 16 ? 2 : 1;
   // One CTA fills an SM.  A small batch takes no more CTAs than give every warp about two tiles (were all contexts as
   // long as they may be), and a multiple of its segments, so that equal lengths are cut where CTAs meet or not at
   // all: joining across CTAs costs about 4 us.  (One sequence of 300 tokens, 8 KV heads: 8 CTAs 7 us, 20 CTAs 8.8 us.)
   const int64_t segs = std::max<int64_t>(1, (int64_t)batch * Hkv);
   const int64_t tiles = segs * ((max_context_len + (int64_t)kTile - 1) / kTile);
-  const int64_t sms = sm_count(), want = (tiles + 2 * kWarps - 1) / (2 * kWarps);
+  const int64_t sms = sm_count() / HV, want = (tiles + 2 * kWarps - 1) / (2 * kWarps);
   int64_t grid = std::min(sms, std::max<int64_t>(1, want));
   if (segs <= sms) {
     const int64_t up = std::min(sms / segs, (grid + segs - 1) / segs) * segs;
     if (up >= grid || up * 20 >= grid * 19) grid = up;
   }
-  pl->grid = std::min(num_partitions ? num_partitions : (int)grid, kMaxGrid);
+  if (num_partitions) grid = (num_partitions + (int64_t)HV - 1) / HV;
+  pl->grid = (int)std::min<int64_t>(grid, kMaxGrid / HV) * HV;
   auto align256 = [](size_t x) { return (x + 255) & ~size_t(255); };
   const size_t slots = (size_t)batch * Hkv + pl->grid;
   pl->off_r = 3 * kMaxGrid * 4;
@@ -1215,12 +1190,12 @@ bool make_plan(int batch, int Hq, int Hkv, int D, int max_context_len, int num_p
   return true;
 }
 
-template <int DT, int D, int G>
+template <int DT, int D, int G, int HV = 1>
 int launch(const Params& p, int grid, cudaStream_t st) {
   constexpr int NW = Shape<D, G>::NW, NS = Shape<D, G>::NS;
   using LY = Layout<D, G, NW, NS>;
   static_assert(LY::BYTES <= 227 * 1024, "shared memory of one CTA");
-  auto kern = decode_int4_kernel<DT, D, G, NW, NS>;
+  auto kern = decode_int4_kernel<DT, D, G, HV, NW, NS>;
   // per instantiation and device; host threads may race to set it, which only repeats an idempotent call
   static std::atomic<bool> attr_set[64] = {};
   int dev = 0;
@@ -1240,7 +1215,7 @@ int dispatch_g(int G, const Params& p, int grid, cudaStream_t st) {
     case 2: return launch<DT, D, 2>(p, grid, st);
     case 4: return launch<DT, D, 4>(p, grid, st);
     case 8: return launch<DT, D, 8>(p, grid, st);
-    case 16: return launch<DT, D, 16>(p, grid, st);
+    case 16: return launch<DT, D, 8, 2>(p, grid, st);
   }
   return PA_ERR_UNSUPPORTED;
 }
