@@ -612,6 +612,7 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
   long long* warp_tiles = reinterpret_cast<long long*>(smem + LY::SCAN_OFF);
   int* warp_longest = reinterpret_cast<int*>(smem + LY::LONG_OFF);
   long long* incl_s = reinterpret_cast<long long*>(smem + LY::INCL_OFF);
+  long long* cut_s = reinterpret_cast<long long*>(smem + LY::PART_OFF);  // [2], at the start
   Piece* pieces = reinterpret_cast<Piece*>(smem + LY::PIECE_OFF);
   int* lens_s = reinterpret_cast<int*>(smem + LY::LENS_OFF);
   const int B = p.batch, Hkv = p.num_kv_heads, bs = p.block_size;
@@ -656,32 +657,34 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
     }
   }
   __syncthreads();
-  long long wincl = lane < NW ? warp_tiles[lane] : 0;  // places (per KV head) up to and with warp `lane`'s sequences
+  long long wincl = lane < NW ? warp_tiles[lane] * Hkv : 0;  // places up to and with warp `lane`'s sequences
 #pragma unroll
   for (int o = 1; o < NW; o <<= 1) {
     const long long t = __shfl_up_sync(0xffffffffu, wincl, o);
     if (lane >= o) wincl += t;
   }
-  const long long total = __shfl_sync(0xffffffffu, wincl, NW - 1) * Hkv;
+  const long long total = __shfl_sync(0xffffffffu, wincl, NW - 1);
   const long long ctas = min((long long)line_ctas, total);
   const bool narrow = (total + 1) * (ctas + 1) < (1ll << 32);
   // The segment at place x of the line, and the tile (the segment's first one, if x is one of its kStart places).
   auto find = [&](long long x) {
     Walk w = {};
-    const long long y = udiv(x, Hkv, narrow);  // per KV head
-    const int wsel = __popc(__ballot_sync(0xffffffffu, lane < NW && wincl <= y));
+    const int wsel = __popc(__ballot_sync(0xffffffffu, lane < NW && wincl <= x));
     const long long before = wsel ? __shfl_sync(0xffffffffu, wincl, wsel - 1) : 0;
-    const long long li = incl_s[wsel * 32 + lane] + before;
-    const int tsel = __popc(__ballot_sync(0xffffffffu, li <= y));
-    long long pre = tsel ? __shfl_sync(0xffffffffu, li, tsel - 1) : before;
+    const long long li = incl_s[wsel * 32 + lane] * Hkv + before;
+    const int tsel = __popc(__ballot_sync(0xffffffffu, li <= x));
+    long long in_seq = x - (tsel ? __shfl_sync(0xffffffffu, li, tsel - 1) : before);
     w.b = (wsel * 32 + tsel) * per;
     for (;; ++w.b) {
       w.L = len_of(w.b);
-      if (pre + places_of(w.L) > y) break;
-      pre += places_of(w.L);
+      const long long all = (long long)places_of(w.L) * Hkv;
+      if (in_seq < all) break;
+      in_seq -= all;
     }
-    const long long in_seq = x - pre * Hkv;
-    w.g = (int)udiv(in_seq, places_of(w.L), narrow);
+    // a quotient below Hkv, from one in floating point that is off by less than 1
+    w.g = min((int)__fdividef((float)in_seq, (float)places_of(w.L)), Hkv - 1);
+    const long long rest = in_seq - (long long)w.g * places_of(w.L);
+    w.g += rest < 0 ? -1 : (rest >= places_of(w.L) ? 1 : 0);
     const int place = (int)(in_seq - (long long)w.g * places_of(w.L));
     w.seg_start = x - place;
     w.t = max(0, place - kStart);
@@ -702,21 +705,24 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
   if (cta < ctas) {
     long long x0 = udiv(total * cta, ctas, narrow), x1 = udiv(total * (cta + 1), ctas, narrow);
     const int longest = __reduce_max_sync(0xffffffffu, lane < NW ? warp_longest[lane] : 0);
-    if (longest <= kUncut) {  // move the cuts to the nearest ends of segments
-      auto nearest = [&](long long x) {
-        if (x == 0 || x == total) return x;
-        const Walk w = find(x);
-        return 2 * (x - w.seg_start) < places_of(w.L) ? w.seg_start : w.seg_start + places_of(w.L);
-      };
-      x0 = nearest(x0);
-      x1 = nearest(x1);
-    }
-    const long long xs = x0 + (x1 - x0) * warp / NW, xe = x0 + (x1 - x0) * (warp + 1) / NW;
-    if (xs < xe) {
-      w0 = find(xs);
-      w0.line_end = xe;
-      // a part that ends in a segment's kStart places, or starts behind its last tile, may hold no tile of it
-      any = w0.t < xe - w0.seg_start - kStart;
+    // first (where segments are short) even warps move the CTA's first cut to the nearest end of a segment, odd ones its
+    // last; then each warp looks its own part up.  One copy of the search: its instructions come from far.
+#pragma unroll 1
+    for (bool cuts = longest <= kUncut;; cuts = false) {
+      const long long xs = x0 + (x1 - x0) * warp / NW, xe = x0 + (x1 - x0) * (warp + 1) / NW;
+      const long long x = cuts ? (warp & 1 ? x1 : x0) : xs;
+      if (cuts || xs < xe) w0 = find(min(x, total - 1));
+      if (!cuts) {
+        w0.line_end = xe;
+        // a part that ends in a segment's kStart places, or starts behind its last tile, may hold no tile of it
+        any = xs < xe && w0.t < xe - w0.seg_start - kStart;
+        break;
+      }
+      const long long next = w0.seg_start + places_of(w0.L);
+      if (lane == 0 && warp < 2) cut_s[warp] = 2 * (x - w0.seg_start) < places_of(w0.L) ? w0.seg_start : next;
+      __syncthreads();
+      x0 = cut_s[0];
+      x1 = cut_s[1];
     }
   }
   __syncthreads();  // the scans are done with: the windows take their place
