@@ -41,6 +41,11 @@
 //     stays if it puts the first tile's largest P' into [2^3, 2^15) and is set so (to (2^3, 2^4]) otherwise; later R
 //     is raised only when P' come near 2^15 or the sum l passes 2^100.  Any R gives the same quotient O / l;
 //     the usual tile needs no maximum, no shuffles and no rescaling of O, one vote tells.  l and O are fp32.
+//
+// Measured (B200): 64 sequences of 4096 to 8192 tokens, 64 heads, 8 KV heads of 128 (455 MB): 92 us, 4.9 TB/s, in bursts,
+// 101 at the power limit; the tiles go by at 6 TB/s.  128 sequences of 100 to 1024, 16 heads (84 MB): 24.5 us, of which
+// 3 until the first loads, 2 until they land, 14 at 6 TB/s and 4 to 5 until the last CTA has joined its pieces.  One sequence
+// of 100001, 32 heads, 2 KV heads: 23.6 us.  4 sequences of up to 64 tokens: 3.8 us.
 
 #include <algorithm>
 #include <atomic>
