@@ -115,7 +115,7 @@ struct Queued {
 // The walk of a warp between two windows of block lookups (kept in shared memory: it is looked at once in 16 tiles).
 struct Walk {
   int b, g, L, t;       // segment, its length, next tile
-  int end, pad;         // where the piece ends
+  int end, item;        // where the piece ends; dealt segments: which of the CTA's it is (else -1)
   long long seg_start;  // where the segment starts on the line, and where the warp's part of the line ends
   long long line_end;
 };
@@ -151,7 +151,8 @@ struct Layout {
   // q rows of the pieces filed, for groups of heads small enough: their pieces may be short, and each would wait for q
   static constexpr bool QS = G <= 4;
   static constexpr int QB = QS ? G * D * 2 : 0;
-  static constexpr int QS_OFF = LENS_OFF + kLens * 4;            // QB [NW][NQ]
+  static constexpr int ITEMS_OFF = LENS_OFF + kLens * 4;         // int2 [32]: sequence and KV head of the segments dealt to the CTA
+  static constexpr int QS_OFF = ITEMS_OFF + 256;                 // QB [NW][NQ]
   static constexpr int BYTES = QS_OFF + NW * NQ * QB;
   // Byte offset of word `word` (4 bytes) of row `row` among a tile's codes: 16-byte units of a row are exchanged so
   // that neighbouring rows' units lie in different banks.  Rows 8 apart are exchanged alike.
@@ -618,6 +619,11 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
   int* warp_longest = reinterpret_cast<int*>(smem + LY::LONG_OFF);
   long long* incl_s = reinterpret_cast<long long*>(smem + LY::INCL_OFF);
   long long* cut_s = reinterpret_cast<long long*>(smem + LY::PART_OFF);  // [2], at the start
+  int* order = reinterpret_cast<int*>(smem + LY::PART_OFF);              // [NW * 32], at the start
+  int* hist = order + NW * 32;  // [NW][32]: a warp's sequences of 32, 31, .. 1 tiles
+  static_assert(NW * 256 <= NW * LY::PART, "room for order and hist");
+  static_assert(kUncut <= 32, "bins of hist");
+  int2* items = reinterpret_cast<int2*>(smem + LY::ITEMS_OFF);
   Piece* pieces = reinterpret_cast<Piece*>(smem + LY::PIECE_OFF);
   int* lens_s = reinterpret_cast<int*>(smem + LY::LENS_OFF);
   const int B = p.batch, Hkv = p.num_kv_heads, bs = p.block_size;
@@ -637,6 +643,8 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
   auto len_of = [&](int i) { return i < kLens ? lens_s[i] : min(max(__ldg(p.context_lens + i), 0), cap); };
   auto tiles_of = [](int L) { return (L + kTile - 1) / kTile; };
   auto places_of = [](int L) { return L > 0 ? (L + kTile - 1) / kTile + kStart : 0; };
+  int my_tiles;    // of sequence `thread`, where every thread has one at most
+  unsigned alike;  // the warp's lanes with as many
   {
     long long incl = 0;
     int longest = 0;
@@ -648,6 +656,11 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
       incl += places_of(Lc);
       longest = max(longest, tiles_of(Lc));
     }
+    my_tiles = tiles_of(threadIdx.x < B && per == 1 ? lens_s[threadIdx.x] : 0);
+    hist[warp * 32 + lane] = 0;
+    __syncwarp();
+    alike = __match_any_sync(0xffffffffu, my_tiles);
+    if (my_tiles > 0 && my_tiles <= 32 && lane == __ffs(alike) - 1) hist[warp * 32 + 32 - my_tiles] = __popc(alike);
     if (clamped && blockIdx.x == 0) PA_RECORD_ERROR(PA_ERRBIT_INDEX);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -674,6 +687,7 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
   // The segment at place x of the line, and the tile (the segment's first one, if x is one of its kStart places).
   auto find = [&](long long x) {
     Walk w = {};
+    w.item = -1;
     const int wsel = __popc(__ballot_sync(0xffffffffu, lane < NW && wincl <= x));
     const long long before = wsel ? __shfl_sync(0xffffffffu, wincl, wsel - 1) : 0;
     const long long li = incl_s[wsel * 32 + lane] * Hkv + before;
@@ -699,7 +713,12 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
   auto step_on = [&](Walk& w) {
     w.seg_start += places_of(w.L);
     w.t = 0;
-    if (++w.g == p.num_kv_heads) {
+    if (w.item >= 0) {
+      const int2 it = items[++w.item];
+      w.b = it.x;
+      w.g = it.y;
+      w.L = len_of(w.b);
+    } else if (++w.g == p.num_kv_heads) {
       w.g = 0;
       do w.L = len_of(++w.b);
       while (w.L == 0 && w.b < p.batch - 1);
@@ -707,9 +726,50 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
   };
   Walk w0 = {};  // this warp's part of the line: from w0 to w0.line_end
   bool any = false;
-  if (cta < ctas) {
+  const int longest = __reduce_max_sync(0xffffffffu, lane < NW ? warp_longest[lane] : 0);
+  if (longest <= kUncut && B <= NW * 32 && (long long)B * Hkv <= 32ll * line_ctas) {
+    // ---- dealt: the segments by falling length, to the CTAs in turn and back again; a CTA's are its line
+    int before = 0, all = 0;  // sequences of 32 - lane tiles: in the warps before this one, and in all
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const int n = hist[w * 32 + lane];
+      before += w < warp ? n : 0;
+      all += n;
+    }
+    int longer = all;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, longer, o);
+      if (lane >= o) longer += t;
+    }
+    const int seqs = __shfl_sync(0xffffffffu, longer, 31);  // that are not empty
+    const int rank0 = __shfl_sync(0xffffffffu, longer - all + before, my_tiles ? 32 - my_tiles : 0);
+    if (my_tiles) order[rank0 + __popc(alike & ((1u << lane) - 1u))] = threadIdx.x;
+    __syncthreads();
+    const int k = lane * line_ctas + (lane & 1 ? line_ctas - 1 - cta : cta);  // the CTA's segment `lane`
+    const bool have = k < seqs * Hkv;
+    const int rank = have ? k / Hkv : 0, kvh = k - rank * Hkv, b = have ? order[rank] : 0, L = have ? lens_s[b] : 0;
+    int incl = places_of(L);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    if (warp == 0 && have) items[lane] = make_int2(b, kvh);
+    const int own = __shfl_sync(0xffffffffu, incl, 31), xs = own * warp / NW, xe = own * (warp + 1) / NW;
+    if (xs < xe) {
+      const int at = __popc(__ballot_sync(0xffffffffu, incl <= xs));
+      w0.b = __shfl_sync(0xffffffffu, b, at);
+      w0.g = __shfl_sync(0xffffffffu, kvh, at);
+      w0.L = __shfl_sync(0xffffffffu, L, at);
+      w0.seg_start = __shfl_sync(0xffffffffu, incl, at) - places_of(w0.L);
+      w0.t = max(0, xs - (int)w0.seg_start - kStart);
+      w0.line_end = xe;
+      w0.item = at;
+      any = w0.t < xe - (int)w0.seg_start - kStart;
+    }
+  } else if (cta < ctas) {
     long long x0 = udiv(total * cta, ctas, narrow), x1 = udiv(total * (cta + 1), ctas, narrow);
-    const int longest = __reduce_max_sync(0xffffffffu, lane < NW ? warp_longest[lane] : 0);
     // first (where segments are short) even warps move the CTA's first cut to the nearest end of a segment, odd ones its
     // last; then each warp looks its own part up.  One copy of the search: its instructions come from far.
 #pragma unroll 1
