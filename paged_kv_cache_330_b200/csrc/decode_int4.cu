@@ -6,9 +6,10 @@
 // hold 256.  At that size the work per byte, not HBM, is what has to be kept small, so the kernel is built
 // around warps that never wait for one another.
 //
-// Work split.  A segment is one (sequence, KV head), cut into tiles of 32 tokens.  On a line of all segments end to
-// end, a segment takes kStart places for what starting and ending it costs, then a place per tile.  CTA c takes places
-// [T c / n, T (c+1) / n) of T (moved to the ends of segments where these are short), its warps equal parts of that.
+// Work split.  A segment is one (sequence, KV head), cut into tiles of 32 tokens; on a line of segments end to end it takes
+// kStart places for what starting and ending it costs, then a place per tile.  Where segments are many and not long
+// they are dealt to the CTAs whole, by falling length to and fro, and what a CTA gets is its line.  Otherwise there is one
+// line of all segments, and CTA c takes places [T c / n, T (c+1) / n) of T.  A CTA's warps take equal parts of its line.
 // Every warp walks its own part: it looks its blocks up, brings its tiles into a ring of its own with asynchronous
 // 16-byte copies (cp.async, nine a lane per tile; no other warp involved) and keeps the softmax state and the output
 // of the current segment in registers.  Bulk copies were measured first: one instruction per copy, but each of a
@@ -43,8 +44,8 @@
 //     the usual tile needs no maximum, no shuffles and no rescaling of O, one vote tells.  l and O are fp32.
 //
 // Measured (B200): 64 sequences of 4096 to 8192 tokens, 64 heads, 8 KV heads of 128 (455 MB): 92 us, 4.9 TB/s, in bursts,
-// 101 at the power limit; the tiles go by at 6 TB/s.  128 sequences of 100 to 1024, 16 heads (84 MB): 24.5 us, of which
-// 3 until the first loads, 2 until they land, 14 at 6 TB/s and 4 to 5 until the last CTA has joined its pieces.  One sequence
+// 101 at the power limit; the tiles go by at 6 TB/s.  128 sequences of 100 to 1024, 16 heads (84 MB): 22.2 us, of which
+// 3 until the first loads, 2 until they land, 14 at 6 TB/s and 2 to 3 until the last CTA has joined its pieces.  One sequence
 // of 100001, 32 heads, 2 KV heads: 23.6 us.  4 sequences of up to 64 tokens: 3.8 us.
 
 #include <algorithm>
@@ -60,13 +61,20 @@ namespace {
 using namespace pa;
 
 constexpr int kTile = 32;            // tokens per tile: two 16-token chunks, each within one block
-constexpr int kStart = 1;            // what a segment costs besides its tiles, in tiles
+// What a segment costs besides its tiles, in tiles: 256 sequences of 16 to 300 tokens 18.5 us with 1, 17.6 with 2, 17.7
+// with 3; 128 of 100 to 1024 22.4, 22.2, 22.2; 40 of 100 to 4096 26.7, 26.8, 27.1.
+constexpr int kStart = 2;
 constexpr int kLens = 512;           // sequences whose lengths a CTA keeps in shared memory
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kGroup = 8;            // CTAs whose shares of a segment are joined first, where a segment has many
-// Segments of up to so many tiles are not cut between CTAs.  A CTA then holds up to one segment more or less than its
-// share, about 0.11 us a tile (D 128, 12 warps); joining a segment across CTAs costs about 5 us at the end.
-constexpr int kUncut = 32;
+// Segments of up to kUncut tiles are dealt whole to the CTAs where the CTAs that get one less than the others wait for less
+// than kJoin tiles, on the mean: joining a segment across CTAs costs about 5 us at the end, a tile 0.11 us (D 128).  Dealt
+// against cut: 32 sequences of 1000 to 2048 tokens (256 segments) 19.1 and 22.1 us, 64 of 500 to 8000 (D 64, 256 segments)
+// 24.2 and 28.3; 16 segments of 63 tiles on 48 CTAs, where 43 tiles would be waited for, 13.4 and 11.5.  Where
+// there are too many to deal, those of up to kMove tiles are not cut either: the CTAs' cuts move to their ends.
+constexpr int kUncut = 256, kMove = 32;
+template <int D>
+constexpr int kJoin = D == 128 ? 30 : 60;
 // CTAs of a grid, at most.  The counters' room is this large whatever the sizes, so that a workspace serves calls of
 // any sizes in turn: nothing of one call's results lies where the next one counts.
 constexpr int kMaxGrid = 1024;
@@ -160,7 +168,7 @@ struct Layout {
     const int unit = word >> 2;
     return row * ROWB + ((ROWB == 64 ? unit ^ (row >> 1 & 3) : unit ^ (row >> 2 & 1)) << 4) + (word & 3) * 4;
   }
-  static_assert(STAGE % 128 == 0 && sizeof(Piece) % 8 == 0 && sizeof(Queued) == 32 && sizeof(Walk) == 40 && PIECE_OFF % 16 == 0 && QUEUE_OFF % 16 == 0 &&
+  static_assert(STAGE % 128 == 0 && sizeof(Piece) % 8 == 0 && sizeof(Queued) == 32 && sizeof(Walk) == 40 && ITEMS_OFF % 8 == 0 && PIECE_OFF % 16 == 0 && QUEUE_OFF % 16 == 0 &&
                     WIN_OFF % 16 == 0 && CONV_OFF % 16 == 0 && CONV % 16 == 0,
                 "alignment");
 };
@@ -618,11 +626,10 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
   long long* warp_tiles = reinterpret_cast<long long*>(smem + LY::SCAN_OFF);
   int* warp_longest = reinterpret_cast<int*>(smem + LY::LONG_OFF);
   long long* incl_s = reinterpret_cast<long long*>(smem + LY::INCL_OFF);
-  long long* cut_s = reinterpret_cast<long long*>(smem + LY::PART_OFF);  // [2], at the start
-  int* order = reinterpret_cast<int*>(smem + LY::PART_OFF);              // [NW * 32], at the start
-  int* hist = order + NW * 32;  // [NW][32]: a warp's sequences of 32, 31, .. 1 tiles
+  long long* cut_s = reinterpret_cast<long long*>(smem + LY::ITEMS_OFF);  // [2], where nothing is dealt
+  int* order = reinterpret_cast<int*>(smem + LY::PART_OFF);  // [NW * 32], at the start: the sequences by falling length
+  int* hist = order + NW * 32;                               // [NW][32]: a warp's sequences by bin, the longest first
   static_assert(NW * 256 <= NW * LY::PART, "room for order and hist");
-  static_assert(kUncut <= 32, "bins of hist");
   int2* items = reinterpret_cast<int2*>(smem + LY::ITEMS_OFF);
   Piece* pieces = reinterpret_cast<Piece*>(smem + LY::PIECE_OFF);
   int* lens_s = reinterpret_cast<int*>(smem + LY::LENS_OFF);
@@ -643,8 +650,6 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
   auto len_of = [&](int i) { return i < kLens ? lens_s[i] : min(max(__ldg(p.context_lens + i), 0), cap); };
   auto tiles_of = [](int L) { return (L + kTile - 1) / kTile; };
   auto places_of = [](int L) { return L > 0 ? (L + kTile - 1) / kTile + kStart : 0; };
-  int my_tiles;    // of sequence `thread`, where every thread has one at most
-  unsigned alike;  // the warp's lanes with as many
   {
     long long incl = 0;
     int longest = 0;
@@ -656,11 +661,6 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
       incl += places_of(Lc);
       longest = max(longest, tiles_of(Lc));
     }
-    my_tiles = tiles_of(threadIdx.x < B && per == 1 ? lens_s[threadIdx.x] : 0);
-    hist[warp * 32 + lane] = 0;
-    __syncwarp();
-    alike = __match_any_sync(0xffffffffu, my_tiles);
-    if (my_tiles > 0 && my_tiles <= 32 && lane == __ffs(alike) - 1) hist[warp * 32 + 32 - my_tiles] = __popc(alike);
     if (clamped && blockIdx.x == 0) PA_RECORD_ERROR(PA_ERRBIT_INDEX);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -727,9 +727,17 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
   Walk w0 = {};  // this warp's part of the line: from w0 to w0.line_end
   bool any = false;
   const int longest = __reduce_max_sync(0xffffffffu, lane < NW ? warp_longest[lane] : 0);
-  if (longest <= kUncut && B <= NW * 32 && (long long)B * Hkv <= 32ll * line_ctas) {
-    // ---- dealt: the segments by falling length, to the CTAs in turn and back again; a CTA's are its line
-    int before = 0, all = 0;  // sequences of 32 - lane tiles: in the warps before this one, and in all
+  bool dealt = longest <= kUncut && B <= NW * 32 && (long long)B * Hkv <= 32ll * line_ctas;
+  int segs = 0;
+  if (dealt) {  // order the sequences by falling length, in 32 bins (31 - length / width; 32: empty), by place within one
+    const int width = (longest + 31) / 32, mine = threadIdx.x < B ? tiles_of(lens_s[threadIdx.x]) : 0;
+    const int my_bin = mine ? 31 - (mine - 1) / width : 32;
+    const unsigned alike = __match_any_sync(0xffffffffu, my_bin);
+    hist[warp * 32 + lane] = 0;
+    __syncwarp();
+    if (my_bin < 32 && lane == __ffs(alike) - 1) hist[warp * 32 + my_bin] = __popc(alike);
+    __syncthreads();
+    int before = 0, all = 0;  // sequences in bin `lane`: in the warps before this one, and in all
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
       const int n = hist[w * 32 + lane];
@@ -743,11 +751,16 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
       if (lane >= o) longer += t;
     }
     const int seqs = __shfl_sync(0xffffffffu, longer, 31);  // that are not empty
-    const int rank0 = __shfl_sync(0xffffffffu, longer - all + before, my_tiles ? 32 - my_tiles : 0);
-    if (my_tiles) order[rank0 + __popc(alike & ((1u << lane) - 1u))] = threadIdx.x;
+    const int rank0 = __shfl_sync(0xffffffffu, longer - all + before, min(my_bin, 31));
+    if (my_bin < 32) order[rank0 + __popc(alike & ((1u << lane) - 1u))] = threadIdx.x;
+    segs = seqs * Hkv;
     __syncthreads();
+    const int rounds = (segs + line_ctas - 1) / line_ctas;
+    if (segs) dealt = places_of(lens_s[order[(rounds - 1) * line_ctas / Hkv]]) * (rounds * line_ctas - segs) <= kJoin<D> * line_ctas;
+  }
+  if (dealt) {  // to the CTAs in turn and back again; a CTA's segments are its line
     const int k = lane * line_ctas + (lane & 1 ? line_ctas - 1 - cta : cta);  // the CTA's segment `lane`
-    const bool have = k < seqs * Hkv;
+    const bool have = k < segs;
     const int rank = have ? k / Hkv : 0, kvh = k - rank * Hkv, b = have ? order[rank] : 0, L = have ? lens_s[b] : 0;
     int incl = places_of(L);
 #pragma unroll
@@ -773,7 +786,7 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
     // first (where segments are short) even warps move the CTA's first cut to the nearest end of a segment, odd ones its
     // last; then each warp looks its own part up.  One copy of the search: its instructions come from far.
 #pragma unroll 1
-    for (bool cuts = longest <= kUncut;; cuts = false) {
+    for (bool cuts = longest <= kMove;; cuts = false) {
       const long long xs = x0 + (x1 - x0) * warp / NW, xe = x0 + (x1 - x0) * (warp + 1) / NW;
       const long long x = cuts ? (warp & 1 ? x1 : x0) : xs;
       if (cuts || xs < xe) w0 = find(min(x, total - 1));

@@ -305,6 +305,30 @@ def test_decode_int4_large_batches(B):
         _check_decode(wl, cache, bt, ln, ref, f"int4 B{B} partitions{ns}", num_partitions=ns)
 
 
+@pytest.mark.parametrize("B,D", [(383, 128), (384, 128), (385, 128), (511, 64), (512, 64), (513, 64)])
+def test_decode_int4_batches_about_the_threads_of_a_cta(B, D):
+    """Where segments stop being dealt by length, and the counts that are and are not a multiple of four."""
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, 150, B)
+    lens[rng.integers(0, B, 5)] = 700
+    wl = make_custom(seed=B, lens=lens.tolist(), num_q_heads=2, num_kv_heads=1, head_dim=D, block_size=16)
+    host, cache, bt, ln = _pool_step(wl)
+    ref = reference(wl.q, *host, bt, ln, wl.scale)
+    for ns in (0, 3, 12, 16):  # 12 CTAs of 32 segments each at most
+        _check_decode(wl, cache, bt, ln, ref, f"int4 B{B} partitions{ns}", num_partitions=ns)
+
+
+@pytest.mark.parametrize("lens", [[2048] * 20, [1024] * 19, [8192, 8000, 64, 1], [8193, 30, 30], [4000, 100] * 10])
+def test_decode_int4_dealt_and_cut(lens):
+    """Equal and unequal lengths on both sides of the rule that deals segments whole, dealt and cut by the grid given."""
+    wl = make_custom(seed=len(lens), lens=lens, num_q_heads=16, num_kv_heads=2, head_dim=64, block_size=32)
+    host, cache, bt, ln = _pool_step(wl)
+    rows = [(b, h) for b in range(0, len(lens), max(1, len(lens) // 4)) for h in (0, 7, 8, 15)]
+    ref = reference(wl.q, *host, bt, ln, wl.scale, rows)
+    for ns in (0, 2, 20, 38, 148):
+        _check_decode(wl, cache, bt, ln, ref, f"int4 {lens[:3]} partitions{ns}", num_partitions=ns)
+
+
 @pytest.mark.parametrize("Hq,Hkv,D,dtype", [(16, 1, 128, "bf16"), (4, 2, 64, "f16")])
 def test_decode_int4_one_long_sequence(Hq, Hkv, D, dtype):
     wl = make_custom(seed=9, lens=[40001], num_q_heads=Hq, num_kv_heads=Hkv, head_dim=D, block_size=64, dtype=dtype)
