@@ -728,8 +728,9 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
   bool any = false;
   const int longest = __reduce_max_sync(0xffffffffu, lane < NW ? warp_longest[lane] : 0);
   bool dealt = longest <= kUncut && B <= NW * 32 && (long long)B * Hkv <= 32ll * line_ctas;
-  int segs = 0;
-  if (dealt) {  // order the sequences by falling length, in 32 bins (31 - length / width; 32: empty), by place within one
+  const bool one = (long long)B * Hkv <= line_ctas;  // a segment a CTA at most: in any order
+  int segs = B * Hkv, first = 0, last = longest;     // the last round: its first segment, and that one's tiles
+  if (dealt && !one) {  // order the sequences by falling length, in 32 bins (31 - length / width; 32: empty), by place within one
     const int width = (longest + 31) / 32, mine = threadIdx.x < B ? tiles_of(lens_s[threadIdx.x]) : 0;
     const int my_bin = mine ? 31 - (mine - 1) / width : 32;
     const unsigned alike = __match_any_sync(0xffffffffu, my_bin);
@@ -755,13 +756,14 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
     if (my_bin < 32) order[rank0 + __popc(alike & ((1u << lane) - 1u))] = threadIdx.x;
     segs = seqs * Hkv;
     __syncthreads();
-    const int rounds = (segs + line_ctas - 1) / line_ctas;
-    if (segs) dealt = places_of(lens_s[order[(rounds - 1) * line_ctas / Hkv]]) * (rounds * line_ctas - segs) <= kJoin<D> * line_ctas;
+    first = max(segs - 1, 0) / line_ctas * line_ctas;
+    last = segs ? tiles_of(lens_s[order[first / Hkv]]) : 0;
   }
+  dealt = dealt && last * (line_ctas - (segs - first)) <= kJoin<D> * line_ctas;
   if (dealt) {  // to the CTAs in turn and back again; a CTA's segments are its line
     const int k = lane * line_ctas + (lane & 1 ? line_ctas - 1 - cta : cta);  // the CTA's segment `lane`
     const bool have = k < segs;
-    const int rank = have ? k / Hkv : 0, kvh = k - rank * Hkv, b = have ? order[rank] : 0, L = have ? lens_s[b] : 0;
+    const int rank = have ? k / Hkv : 0, kvh = k - rank * Hkv, b = one ? rank : (have ? order[rank] : 0), L = have ? lens_s[b] : 0;
     int incl = places_of(L);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
