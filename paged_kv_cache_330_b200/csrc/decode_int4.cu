@@ -30,7 +30,7 @@
 //     at 2^-24 where the products of normal numbers are cut at 2^-34.  With V that is 2^-14 of the largest weight in 16,
 //     less than the weights' own rounding.  With K it would be 2^-14 of the largest q: errors of 2e-5 in scores of
 //     ordinary size, against 2e-7 with all of K's codes 2^4 higher, in bits 4 to 7.  That costs two multiplications a
-//     word, 2 % of the time (128 sequences 23.8 -> 24.5 us, long ones 99 -> 101 us).
+//     word, 2 % of the time (64 sequences of 4096 to 8192, 99 -> 101 us).
 //   * Parameters are converted once per token (lane = token), not once per lane that needs them, and handed round
 //     through shared memory: s_K times the score scale as fp32, s_V as fp32, both z as fp16.
 //   * Scores: s_t = sum_group s_K (sum code q + z_K sum q).  The zero-point part is one more product per group, of z
@@ -44,9 +44,9 @@
 //     the usual tile needs no maximum, no shuffles and no rescaling of O, one vote tells.  l and O are fp32.
 //
 // Measured (B200): 64 sequences of 4096 to 8192 tokens, 64 heads, 8 KV heads of 128 (455 MB): 92 us, 4.9 TB/s, in bursts,
-// 101 at the power limit; the tiles go by at 6 TB/s.  128 sequences of 100 to 1024, 16 heads (84 MB): 22.2 us, of which
+// 101 to 105 at the power limit; the tiles go by at 6 TB/s.  128 sequences of 100 to 1024, 16 heads (84 MB): 22.4 us, of which
 // 3 until the first loads, 2 until they land, 14 at 6 TB/s and 2 to 3 until the last CTA has joined its pieces.  One sequence
-// of 100001, 32 heads, 2 KV heads: 23.6 us.  4 sequences of up to 64 tokens: 3.8 us.
+// of 100001, 32 heads, 2 KV heads: 23.3 us.  4 sequences of up to 64 tokens: 3.8 us.
 
 #include <algorithm>
 #include <atomic>
@@ -1232,7 +1232,7 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
 // Warps of a CTA (one CTA fills an SM) and stages of each warp's ring.  D 128, G <= 8: 12 warps of 168 registers; 16 warps
 // of 128 need 590 instructions a tile instead of 522 (values kept and fetched again): 64 sequences of 4096 to 8192
 // tokens, 64 heads, take 92.9 us with 16, 89.5 with 12, 101 with 10, 107 with 8.  D 64 fits 16 (27.4 against 28.6 us,
-// 64 sequences of 500 to 8000).  A third stage changes nothing.
+// 64 sequences of 500 to 8000).  A third stage changes nothing.  (Measured with K's codes low in their halves and segments cut.)
 // G 16 as one piece (two column tiles, 8 warps of 250 registers) against two halves on two CTAs: one sequence of 2000
 // tokens 14.7 and 11.3 us, of 100001 26.8 and 23.7, 16 of 8000 26.6 and 25.6, 64 of 100 to 8000 38.7 and 40.1 (D 128, 2
 // KV heads; D 64 10.3 and 9.8 to 27.7 and 29.4).  Halves, for all.
