@@ -589,6 +589,15 @@ def _handle(stream, lead):
     return stream.cuda_stream
 
 
+def _made_for(stream, make, *args, **kw):
+    """A tensor that a call on the given stream is to use: allocated (and filled) in that stream's order, not the current
+    one's, so that its memory is neither still in use elsewhere nor given to others before the call is done with it."""
+    if stream is None:
+        return make(*args, **kw)
+    with _torch().cuda.stream(stream):
+        return make(*args, **kw)
+
+
 def _int4_caches(k_codes, v_codes, k_params, v_params):
     """Codes uint8 [NB, Hkv, bs, D/2] (both alike), parameters [NB, Hkv, bs, D/64, 2] (both alike, bf16 or fp16):
     words what is wrong with them, if anything is; returns (NB, bs, Hkv, D)."""
@@ -631,7 +640,7 @@ def rope_write_kv_int4(q, k, v, positions, cos_table, sin_table, slot_mapping, k
     their slots.  Returns q_out (a new tensor unless given; q_out=q rotates in place).  k_out, v_out as in
     write_kv_int4."""
     if q_out is None:
-        q_out = _torch().empty_like(q)
+        q_out = _made_for(stream, _torch().empty_like, q)
     st = _native().rope_write_kv_int4(q, k, v, positions, cos_table, sin_table, slot_mapping, k_codes, v_codes, k_params,
                                      v_params, q_out, k_out, v_out, _handle(stream, q))
     if st == _WRONG:
@@ -703,14 +712,14 @@ def decode_int4(q, k_codes, v_codes, k_params, v_params, block_tables, context_l
     """Decode over the INT4 cache: q [B, Hq, D] in the parameters' dtype; returns out [B, Hq, D].  lse (float32
     [B, Hq], optional) receives the log-sum-exp of each (sequence, head)'s scores, as decode_lse gives it."""
     if out is None:
-        out = _torch().empty_like(q)
+        out = _made_for(stream, _torch().empty_like, q)
     handle = _handle(stream, q)
     call = _native().decode_int4
     st = call(q, k_codes, v_codes, k_params, v_params, block_tables, context_lens, max_context_len, scale, out, lse,
               workspace, num_partitions, handle)
     if st == _NEEDS_WORKSPACE:  # zero-filled once; every call leaves it zeroed again (a given one the library checks)
         need = decode_int4_plan(q.shape[0], q.shape[1], k_codes.shape[1], q.shape[2], max_context_len, num_partitions)[2]
-        workspace = _torch().zeros(need, dtype=_torch().uint8, device=q.device)
+        workspace = _made_for(stream, _torch().zeros, need, dtype=_torch().uint8, device=q.device)
         st = call(q, k_codes, v_codes, k_params, v_params, block_tables, context_lens, max_context_len, scale, out, lse,
                   workspace, num_partitions, handle)
     if st == _WRONG:

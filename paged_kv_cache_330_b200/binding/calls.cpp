@@ -2,7 +2,7 @@
 //
 // On the device these calls take 2 to 6 us for a decode step's few rows.  Through ctypes one costs the host about
 // 10 us (checking the attributes of nine tensors one by one in Python 5 us, converting 16 to 24 arguments 1.3 us, the
-// launch 2.9 us); through this module about 4 us.  Each function takes tensors, reads their types, shapes, strides and
+// launch 2.9 us); through this module about 3 us.  Each function takes tensors, reads their types, shapes, strides and
 // addresses here, and calls the C entry it is bound to.  It returns the entry's status, or kWrong if an argument is
 // not as it has to be (nothing is called; the Python side then finds the words), or kWorkspace if decode is to get a
 // workspace first.  No exception leaves a function.

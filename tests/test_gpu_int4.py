@@ -444,6 +444,36 @@ def test_decode_int4_bad_block_sets_index_bit():
     assert pa.device_error() == 2
 
 
+def test_int4_cache_of_more_than_32_bits_of_bytes():
+    """Blocks on both sides of byte 2^32 of the codes (40000 blocks of 128 KiB): write, copy, decode and expansion give
+    what a cache of a few blocks gives, bit for bit."""
+    Hkv, bs, D, NB, dt = 8, 256, 128, 40000, torch.bfloat16
+    if torch.cuda.mem_get_info()[0] < 20 << 30:
+        pytest.skip("needs 20 GB of free device memory")
+    far = [3, 32767, 32768, NB - 2, NB - 1]
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    T = 4 * bs
+    k, v = (torch.randn(T, Hkv, D, generator=gen, device="cuda").to(dt) for _ in "kv")
+    q = torch.randn(2, 16, D, generator=gen, device="cuda").to(dt)
+    lens = torch.tensor([3 * bs + 17, 2 * bs], dtype=torch.int32, device="cuda")
+    got = []
+    for blocks, n in ((far, NB), ([0, 1, 2, 3, 4], 5)):
+        cache = empty_cache(n, Hkv, bs, D, dt)
+        slots = torch.cat([torch.arange(bs) + b * bs for b in blocks[:4]]).cuda()
+        pa.write_kv_int4(k, v, slots, *cache)
+        pa.copy_blocks_int4(torch.tensor([[blocks[3], blocks[4]]], dtype=torch.int32, device="cuda"), *cache)
+        tables = torch.tensor([[blocks[1], blocks[0], blocks[2], blocks[4]], [blocks[3], blocks[2], -1, -1]],
+                              dtype=torch.int32, device="cuda")
+        out = pa.decode_int4(q, *cache, tables, lens, 4 * bs, D ** -0.5)
+        k16 = torch.zeros(2, bs, Hkv, D, dtype=dt, device="cuda")
+        v16 = torch.zeros_like(k16)
+        pa.load_blocks_int4(torch.tensor([[blocks[4], 0], [blocks[1], 1]], dtype=torch.int32, device="cuda"), *cache, k16, v16)
+        got.append((out, k16, v16))
+        del cache
+    assert pa.device_error() == 0
+    assert all(torch.equal(a, b) for a, b in zip(*got)) and got[0][1].any()
+
+
 # ------------------------------------------------------------------------------------------ streams, graphs, workspaces
 def test_decode_int4_one_workspace_for_calls_of_all_sizes():
     """A workspace zero-filled once and used by calls of other batches, heads, dimensions and work splits in turn, each
@@ -505,6 +535,38 @@ def test_decode_int4_graph_replay_and_side_stream():
         torch.cuda.synchronize()
         assert torch.equal(out, want)
         assert (ws[: 4 * 5 * 8] == 0).all()  # the counters of 5 sequences x 8 KV heads
+
+
+def test_decode_int4_given_stream_without_workspace_while_the_current_one_is_behind():
+    """What a call makes itself (out, the zero-filled workspace, q_out) follows the stream it is given: the current
+    stream is busy, and memory of the workspace's size that it has just freed holds no zeros."""
+    wl = make_custom(seed=43, lens=[9000, 1, 4000], num_q_heads=8, num_kv_heads=1, head_dim=128, block_size=16)
+    host, cache, bt, lens = _pool_step(wl)
+    dev = torch.from_numpy(bt).cuda(), torch.from_numpy(lens).cuda()
+    q = wl.q.cuda()
+    want = pa.decode_int4(q, *cache, *dev, 9000, wl.scale)
+    need = pa.decode_int4_plan(3, 8, 1, 128, 9000)[2]
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        torch.cuda.synchronize()
+        junk = [torch.full((need,), 1, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)  # 10 ms of the current stream
+        del junk
+        got = pa.decode_int4(q, *cache, *dev, 9000, wl.scale, stream=side)
+        side.synchronize()
+        assert torch.equal(got.cpu(), want.cpu())
+    x = torch.randn(5, 8, 128, device="cuda").to(q.dtype)
+    kv = torch.randn(2, 5, 1, 128, device="cuda").to(q.dtype)
+    pos, slots = torch.arange(5, device="cuda"), torch.full((5,), -1, dtype=torch.int64, device="cuda")
+    angle = torch.rand(16, 64, device="cuda")
+    args = (x, kv[0], kv[1], pos, angle.cos(), angle.sin(), slots, *cache)
+    want = pa.rope_write_kv_int4(*args)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)
+    got = pa.rope_write_kv_int4(*args, stream=side)
+    side.synchronize()
+    assert torch.equal(got.cpu(), want.cpu())
 
 
 def test_decode_int4_two_streams_two_workspaces():
