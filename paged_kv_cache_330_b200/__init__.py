@@ -562,7 +562,7 @@ def decode_int8(q, k_codes, v_codes, k_scales, v_scales, block_tables, context_l
 # ---------------------------------------------------------------------------------------------- INT4 cache
 # These calls are short on the device (2 to 6 us for one decode step's rows), so their arguments are checked and
 # marshalled by the native module _calls (binding/calls.cpp) instead of attribute by attribute here.  It calls the C
-# entry, or says that an argument is not as it has to be; the checkers below then word what is wrong.
+# entry, or says that an argument is not as it has to be; the checks below then word what is wrong.
 _NATIVE = None
 _NATIVE_ENTRIES = ("pa_write_kv_int4", "pa_rope_write_kv_int4", "pa_copy_blocks_int4", "pa_load_blocks_int4",
                    "pa_decode_int4")
