@@ -53,6 +53,7 @@
 
 #include "common.cuh"
 #include "host_common.h"
+#include "join_int4.h"
 
 PA_DEFINE_ERROR_WORD(pa__err_decode_int4)
 
@@ -66,7 +67,6 @@ constexpr int kTile = 32;            // tokens per tile: two 16-token chunks, ea
 constexpr int kStart = 2;
 constexpr int kLens = 512;           // sequences whose lengths a CTA keeps in shared memory
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kGroup = 8;            // CTAs whose shares of a segment are joined first, where a segment has many
 // Segments of up to kUncut tiles are dealt whole to the CTAs where the CTAs that get one less than the others wait for less
 // than kJoin tiles, on the mean: joining a segment across CTAs costs about 5 us at the end, a tile 0.11 us (D 128).  Dealt
 // against cut: 32 sequences of 1000 to 2048 tokens (256 segments) 19.1 and 22.1 us, 64 of 500 to 8000 (D 64, 256 segments)
@@ -75,9 +75,6 @@ constexpr int kGroup = 8;            // CTAs whose shares of a segment are joine
 constexpr int kUncut = 256, kMove = 32;
 template <int D>
 constexpr int kJoin = D == 128 ? 30 : 60;
-// CTAs of a grid, at most.  The counters' room is this large whatever the sizes, so that a workspace serves calls of
-// any sizes in turn: nothing of one call's results lies where the next one counts.
-constexpr int kMaxGrid = 1024;
 constexpr float kGuess = -8.f;       // a piece's first reference: fits when its largest weight * V scale is 2^-5 .. 2^7
 constexpr float kUnit = 16777216.f;  // 2^24: what a code's fp16 subnormal stands for, inverted
 constexpr float kUnitK = 1048576.f;  // 2^20: the same for K's codes
@@ -92,18 +89,13 @@ struct Params {
   long long v_params;
   const int32_t* block_tables;
   const int32_t* context_lens;
-  int* ws_cnt;   // [3 kMaxGrid], zero between calls, see counter_of
+  int* ws_cnt;   // [3 kMaxGrid], zero between calls, see join_round
   float* ws_r;   // [slots][G] reference R of a share
   float* ws_l;   // [slots][G]
   float* ws_o;   // [slots][G][D]
   int max_blocks_per_seq, batch, num_q_heads, num_kv_heads, block_size, num_blocks;
   float scale_log2;
 };
-
-// Which counter a cut segment whose first tile is CTA c0's counts its shares with (a CTA holds the first tile of one cut
-// segment at most), and which one the group of its CTAs from gf on (a CTA holds a later share of one segment at most).
-__device__ __forceinline__ int counter_of(int c0) { return c0; }
-__device__ __forceinline__ int group_counter_of(int c0, int gf) { return gf == c0 ? kMaxGrid + gf : 2 * kMaxGrid + gf; }
 
 enum : int { F_VALID = 1, F_HEAD = 2, F_TAIL = 4 };
 
@@ -225,11 +217,6 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// Floor division of a >= 0 by b > 0; `narrow` (uniform) says both fit in 32 bits: the 64-bit one is a long sequence.
-__device__ __forceinline__ long long udiv(long long a, long long b, bool narrow) {
-  return narrow ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
 // One more at a counter that starts at zero, with device scope: what the block wrote before (its barrier passed) is
@@ -1082,8 +1069,7 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
     if ((lane & 7) == 0 && item < runs * G) md_s[r * G + h] = make_float2(M, den);
   }
   __syncthreads();
-  // columns: a thread takes 4 of a head.  Cut segments first: this CTA's shares of them go to the workspace, slot
-  // segment + CTA (a CTA holds at most one share of a segment, and neighbouring segments share at most one CTA).
+  // columns: a thread takes 4 of a head.  Cut segments first: this CTA's shares of them go to the workspace.
   constexpr int QUADS = G * D / 4;
   const size_t ws_row0 = (size_t)half * (B * (size_t)Hkv + line_ctas) * G;  // each half has slots and counters of its own
   float *ws_r = p.ws_r + ws_row0, *ws_l = p.ws_l + ws_row0, *ws_o = p.ws_o + ws_row0 * D;
@@ -1121,42 +1107,34 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
     }
   };
   columns(0, cuts);
-  // The cut segments (0: of the first run, 1: of the last): lane 0 or 1 of every warp, then all lanes of it.
-  size_t seg = 0;
-  int c0 = 0, n_sh = 0;  // the CTAs that hold shares
+  // The cut segments (0: of the first run, 1: of the last), in lanes 0 and 1 of every warp.
+  Cut cut = {0, 0, 0};
   if (lane < 2 && (lane == 0 ? cut0 : cut1)) {
     const Piece& mine = pieces[__ffs(run_s[lane == 0 ? 0 : runs - 1].mask) - 1];
-    seg = (size_t)mine.b * Hkv + mine.g;
-    const long long tile0 = mine.seg_start + kStart;
-    c0 = (int)udiv((tile0 + 1) * ctas - 1, total, narrow);
-    n_sh = (int)udiv((tile0 + mine.nt) * ctas - 1, total, narrow) - c0 + 1;
+    cut = cut_of((long long)mine.b * Hkv + mine.g, mine.seg_start + kStart, mine.nt, ctas, total, narrow);
   }
-  // A segment with many shares is joined by groups of kGroup CTAs first: one SM reads shares at little more than
-  // 100 GB/s.
-  const int gf = max(c0, cta / kGroup * kGroup);
-  const bool grouped = n_sh > 2 * kGroup;
-  int* cnt = ws_cnt + (grouped ? group_counter_of(c0, gf) : counter_of(c0));
-  int n = grouped ? min(c0 + n_sh, (cta / kGroup + 1) * kGroup) - gf : n_sh;  // shares to join now, from slot0 on
-  size_t slot0 = seg + (grouped ? gf : c0), slots = slot0;
-  int step = 1;
-  bool again = grouped;
   int* done_s = reinterpret_cast<int*>(smem + LY::LENS_OFF);
   if (cuts) {
     __syncthreads();  // the CTA's shares are written
-    if (warp == 0 && lane < 2) done_s[lane] = n > 0 && count_last(cnt, n);
+    if (warp == 0 && lane < 2) {
+      const Round r = join_round(0, cut, cta);
+      done_s[lane] = cut.n > 0 && count_last(ws_cnt + r.counter, r.n);
+    }
   }
   columns(cuts, runs);  // meanwhile the segments that lie within the CTA
   if (!cuts) return;
-  // Cut segments whose shares this CTA counted last: a thread takes 4 columns of a head, 8 shares at a time.
+  // Cut segments whose shares this CTA counted last: a thread takes 4 columns of a head, 8 shares at a time.  Each round
+  // follows from the segment alone: nothing is carried from one segment, or one round, to the next.
   constexpr int PASSES = (QUADS + NW * 32 - 1) / (NW * 32), U = 8;
   for (int which = 0; which < 2; ++which) {
-    for (bool first_level = true;; first_level = false) {
+    Cut k;
+    k.seg = __shfl_sync(0xffffffffu, cut.seg, which);
+    k.c0 = __shfl_sync(0xffffffffu, cut.c0, which);
+    k.n = __shfl_sync(0xffffffffu, cut.n, which);
+    for (int round = 0;; ++round) {
       __syncthreads();
       if (!done_s[which]) break;
-      const int n_ = __shfl_sync(0xffffffffu, n, which), step_ = __shfl_sync(0xffffffffu, step, which);
-      const size_t slot0_ = __shfl_sync(0xffffffffu, slot0, which), slots_ = __shfl_sync(0xffffffffu, slots, which);
-      const size_t seg_ = __shfl_sync(0xffffffffu, seg, which);
-      const bool again_ = __shfl_sync(0xffffffffu, again, which);
+      const Round jr = join_round(round, k, cta);
       float4 acc[PASSES];
       float M[PASSES], den[PASSES];
 #pragma unroll
@@ -1166,15 +1144,15 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
         den[ps] = 0.f;
         const int quad = ps * NW * 32 + threadIdx.x, h = quad / (D / 4), col = quad % (D / 4) * 4;
         if (quad >= QUADS) break;
-        for (int i0 = 0; i0 < n_; i0 += U) {
+        for (int i0 = 0; i0 < jr.n; i0 += U) {
           float r[U], l[U];
           float4 v[U];
 #pragma unroll
           for (int u = 0; u < U; ++u) {
-            const int i = min(i0 + u, n_ - 1);  // share i is in slot0 for i = 0, in slots + i * step for the others
-            const size_t row = (i == 0 ? slot0_ : slots_ + (size_t)i * step_) * G + h;
+            const int i = min(i0 + u, jr.n - 1);
+            const size_t row = (size_t)(i == 0 ? jr.slot0 : jr.slots + (long long)i * jr.step) * G + h;
             r[u] = __ldcg(ws_r + row);
-            l[u] = i0 + u < n_ ? __ldcg(ws_l + row) : 0.f;
+            l[u] = i0 + u < jr.n ? __ldcg(ws_l + row) : 0.f;
             v[u] = __ldcg(reinterpret_cast<const float4*>(ws_o + row * D + col));
           }
           float top = M[ps];
@@ -1193,21 +1171,20 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
           }
         }
       }
-      const bool partial = first_level && again_;
-      if (partial) __syncthreads();  // the group's shares are read: their joint share takes the first one's slot
+      if (jr.again) __syncthreads();  // the group's shares are read: their joint share takes the first one's slot
 #pragma unroll
       for (int ps = 0; ps < PASSES; ++ps) {
         const int quad = ps * NW * 32 + threadIdx.x, h = quad / (D / 4), col = quad % (D / 4) * 4;
         if (quad >= QUADS) break;
-        if (partial) {
-          const size_t row = slot0_ * G + h;
+        if (jr.again) {
+          const size_t row = (size_t)jr.slot0 * G + h;
           *reinterpret_cast<float4*>(ws_o + row * D + col) = acc[ps];
           if (col == 0) {
             ws_r[row] = M[ps];
             ws_l[row] = den[ps];
           }
         } else {
-          const size_t at = head0(seg_) + h;
+          const size_t at = head0((size_t)k.seg) + h;
           const float inv = 1.f / den[ps];
           uint2 u;
           u.x = Elt<DT>::from_f2(acc[ps].x * inv, acc[ps].y * inv);
@@ -1216,14 +1193,12 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
           if (p.lse && col == 0) p.lse[at] = (M[ps] + __log2f(den[ps])) * kLn2;
         }
       }
-      if (!partial) break;
-      // count the groups; the last one joins their joint shares
-      slot0 = seg + c0;
-      slots = seg + c0 / kGroup * kGroup;
-      step = kGroup;
-      n = (c0 + n_sh - 1) / kGroup - c0 / kGroup + 1;
-      __syncthreads();
-      if (warp == 0 && lane == which) done_s[lane] = count_last(ws_cnt + counter_of(c0), n);
+      if (!jr.again) break;
+      __syncthreads();  // the joint share is written
+      if (threadIdx.x == 0) {
+        const Round up = join_round(round + 1, k, cta);
+        done_s[which] = count_last(ws_cnt + up.counter, up.n);
+      }
     }
   }
 }
