@@ -339,8 +339,10 @@ int pa_decode_int8(const void* q, const void* k_codes, const void* v_codes, cons
 /* than the type's scale can say): s = |lo|, z = sign(lo), codes 0.  The    */
 /* codes are taken against the rounded s and z, so those roundings cost at  */
 /* most a shifted range, never an inconsistent value.  4.5 bits per value.  */
-/* Finite values of any size are in the format; a NaN or infinity spoils    */
-/* its own group only.                                                      */
+/* Finite values of any size are in the format.  A NaN or an infinity       */
+/* spoils its own group, all of it: min and max keep a NaN, so s is         */
+/* infinite or NaN and the group stands for nothing finite; other groups   */
+/* keep their values.                                                       */
 /* Layout: codes k_codes, v_codes uint8 [num_blocks][Hkv][block_size][D/2]  */
 /* (head-major, unlike the 16-bit and int8 caches: one head's rows of a     */
 /* block are one contiguous run that one bulk copy fetches).  A row is D/8  */

@@ -11,6 +11,9 @@ token, one KV head) is cut into D / 64 groups; a group stands for s * (code + z)
     code = clip(rint(fp32(fp32(x * fp32(1 / s)) - z)), 0, 15)
     s < 2^-126:  s = |lo|, z = sign(lo), code = 0
 
+min and max keep a NaN, so a group that holds one gets s and z NaN; one that holds an infinity gets s infinite or
+NaN.  A code that is NaN before it is clipped is 0.
+
 numpy's float32 arithmetic is IEEE, so a device kernel that takes the same steps reaches the same codes.
 Stored: codes uint8 [NB, Hkv, bs, D/2]; 8 codes to a 4-byte word, lowest nibble first, word j of a row
 holding values 8 * (j div n) .. + 7 of group j mod n (n = D / 64).  Parameters [NB, Hkv, bs, n, 2] = (s, z).
@@ -34,14 +37,14 @@ def quantize_rows(x: torch.Tensor):
     g = xf.reshape(*xf.shape[:-1], xf.shape[-1] // GROUP, GROUP)
     lo, hi = g.min(-1), g.max(-1)
     fifteen = np.float32(15)
-    s = _round16(hi / fifteen - lo / fifteen, x.dtype)
-    alike = s < np.float32(2.0 ** -126)
     with np.errstate(divide="ignore", invalid="ignore", over="ignore"):
+        s = _round16(hi / fifteen - lo / fifteen, x.dtype)
+        alike = s < np.float32(2.0 ** -126)  # not where s is NaN
         z = _round16(np.where(alike, np.sign(lo), lo / np.where(alike, np.float32(1), s)), x.dtype)
         inv = np.float32(1) / np.where(alike, np.float32(1), s)
+        code = np.rint((g * inv[..., None]).astype(np.float32) - z[..., None])
     s = np.where(alike, np.abs(lo), s).astype(np.float32)
-    code = np.rint((g * inv[..., None]).astype(np.float32) - z[..., None])
-    code = np.where(alike[..., None], 0, np.clip(code, 0, 15)).astype(np.uint8)
+    code = np.where(alike[..., None] | np.isnan(code), 0, np.clip(code, 0, 15)).astype(np.uint8)
     return code, s, z
 
 

@@ -17,7 +17,9 @@
 // before the codes are taken, so the rounding shifts the range the codes span
 // but adds nothing to a value's error.  s < 2^-126 (all values alike, or nearer
 // than the type can say; 1 / s would overflow): s = |lo|, z = sign(lo), codes 0.
-// One group never spans tokens: appending a token re-quantises nothing.
+// One group never spans tokens: appending a token re-quantises nothing.  A NaN
+// in a group makes both extremes NaN, and s and z with them; an infinity makes s
+// infinite or NaN.  Either way the group stands for nothing finite.
 //
 // Layout: codes [num_blocks][Hkv][block_size][D/2], parameters
 // [num_blocks][Hkv][block_size][D/64][2].  Word j (8 codes) of a row holds
@@ -78,11 +80,23 @@ __device__ __forceinline__ uint32_t encode8(float* x, float s, float z, float in
   return word;
 }
 
+// The smaller and the larger of two, NaN where either is: fminf and fmaxf would drop it, and with it what went wrong in
+// the values of a group.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
 __device__ __forceinline__ float min8(const float* x) {
-  return fminf(fminf(fminf(x[0], x[1]), fminf(x[2], x[3])), fminf(fminf(x[4], x[5]), fminf(x[6], x[7])));
+  return min_nan(min_nan(min_nan(x[0], x[1]), min_nan(x[2], x[3])), min_nan(min_nan(x[4], x[5]), min_nan(x[6], x[7])));
 }
 __device__ __forceinline__ float max8(const float* x) {
-  return fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+  return max_nan(max_nan(max_nan(x[0], x[1]), max_nan(x[2], x[3])), max_nan(max_nan(x[4], x[5]), max_nan(x[6], x[7])));
 }
 
 struct WriteArgs {
@@ -182,16 +196,16 @@ __global__ void __launch_bounds__(kWriteThreads, 12) write_kv_int4_kernel(const 
     if (ROPE && __all_sync(0xffffffffu, isq || !in)) return;
     float lo1 = min8(x1), hi1 = max8(x1), lo2 = min8(x2), hi2 = max8(x2);
     if constexpr (NG == 1) {
-      lo1 = fminf(lo1, lo2);
-      hi1 = fmaxf(hi1, hi2);
+      lo1 = min_nan(lo1, lo2);
+      hi1 = max_nan(hi1, hi2);
     }
 #pragma unroll
     for (int o = TPR / 2; o > 0; o >>= 1) {
-      lo1 = fminf(lo1, __shfl_xor_sync(0xffffffffu, lo1, o));
-      hi1 = fmaxf(hi1, __shfl_xor_sync(0xffffffffu, hi1, o));
+      lo1 = min_nan(lo1, __shfl_xor_sync(0xffffffffu, lo1, o));
+      hi1 = max_nan(hi1, __shfl_xor_sync(0xffffffffu, hi1, o));
       if constexpr (NG == 2) {
-        lo2 = fminf(lo2, __shfl_xor_sync(0xffffffffu, lo2, o));
-        hi2 = fmaxf(hi2, __shfl_xor_sync(0xffffffffu, hi2, o));
+        lo2 = min_nan(lo2, __shfl_xor_sync(0xffffffffu, lo2, o));
+        hi2 = max_nan(hi2, __shfl_xor_sync(0xffffffffu, hi2, o));
       }
     }
     // Four quotients a group, each an IEEE division: taken by one lane each (two a lane, not eight) and handed round.
@@ -200,7 +214,7 @@ __global__ void __launch_bounds__(kWriteThreads, 12) write_kv_int4_kernel(const 
     const float lo = second ? lo2 : lo1, hi = second ? hi2 : hi1;
     const float q15 = __fdiv_rn(odd ? lo : hi, 15.f), other = __shfl_xor_sync(0xffffffffu, q15, 1);
     float s = Elt<DT>::to_f2(Elt<DT>::from_f2(odd ? __fsub_rn(other, q15) : __fsub_rn(q15, other), 0.f)).x;
-    const bool alike = !(s >= 1.17549435e-38f);
+    const bool alike = s < 1.17549435e-38f;  // a NaN is not: s and z are NaN then, every code 0
     float quot = __fdiv_rn(odd ? 1.f : lo, alike ? 1.f : s);
     if (alike) {
       s = fabsf(lo);

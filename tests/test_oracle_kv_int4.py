@@ -90,3 +90,18 @@ def test_planted_mistakes_are_caught(name):
     held = oq.values(stored, params).reshape(*x.shape[:-1], -1, 64)
     err, bound = _errors(x, held, s, z)
     assert (err > bound).any()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_a_nan_or_infinity_spoils_its_group(dtype):
+    x = _rows(dtype, 5)
+    bad = x.clone()
+    bad[3, 1, 70], bad[5, 0, 2], bad[6, 2, 100], bad[7, 0, 64:] = float("nan"), float("inf"), float("-inf"), float("inf")
+    (code, s, z), (c0, s0, z0) = oq.quantize_rows(bad), oq.quantize_rows(x)
+    lost = np.zeros(s.shape, bool)
+    lost[3, 1, 1] = lost[5, 0, 0] = lost[6, 2, 1] = lost[7, 0, 1] = True
+    with np.errstate(invalid="ignore"):
+        held = s[..., None] * (code + z[..., None])
+    assert not np.isfinite(held[lost]).any() and not np.isfinite(s[lost]).any() and (code[lost] == 0).all()
+    assert np.array_equal(code[~lost], c0[~lost]) and np.array_equal(s[~lost], s0[~lost])
+    assert np.array_equal(z[~lost], z0[~lost])
