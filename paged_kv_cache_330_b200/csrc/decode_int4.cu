@@ -333,7 +333,7 @@ struct State {
   }
 
   // Moves the references of the heads that need it, so that the tile's scores x (relative to R; -inf where
-  // masked) give P' <= 2^4 and l <= 2^91.  svm: the larger V scale of each of this lane's rows.
+  // masked) give P' <= 2^4 and l <= 2^91.  svm: the larger finite V scale of each of this lane's rows.
   __device__ __forceinline__ void rebase(float (&x)[2][4], const float (&svm)[4]) {
     bool still = false;
 #pragma unroll
@@ -524,9 +524,11 @@ struct State {
         fresh = move;
       }
       if (!move || moved) break;
+      // An infinite scale fits with no reference: its group is lost, the other's weights go by its own.
+      auto finite = [](float s) { return s < INFINITY ? s : 0.f; };
       float svm[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) svm[r] = NG == 2 ? fmaxf(sv[r][0], sv[r][NG - 1]) : sv[r][0];
+      for (int r = 0; r < 4; ++r) svm[r] = NG == 2 ? fmaxf(finite(sv[r][0]), finite(sv[r][NG - 1])) : finite(sv[r][0]);
       rebase(x, svm);
     }
     l[0] = sum[0];

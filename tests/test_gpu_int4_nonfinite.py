@@ -138,3 +138,44 @@ def test_decode_int4_nan_in_a_key_reaches_its_heads(Hq, Hkv, D, dt):
         assert np.isnan(o[lost]).all() and np.isnan(l[lost]).all(), ns
         assert_within(o[~lost], out[~lost], bound[~lost], f"beside a NaN key, partitions {ns}")
         assert_within(l[~lost], lse[~lost], lse_bound[~lost], f"beside a NaN key, partitions {ns}, lse")
+
+
+@pytest.mark.parametrize("q_scale", [1.0, 30.0])
+@pytest.mark.parametrize("value", [NAN, INF])
+@pytest.mark.parametrize("Hq,Hkv,dt", [(8, 2, "bf16"), (16, 1, "f16"), (2, 2, "f16")])
+def test_decode_int4_nonfinite_value_reaches_its_group_alone(Hq, Hkv, dt, value, q_scale):
+    """One value row's NaN or infinity (as the writes store a group with one: scale, or scale and zero point, not
+    finite) takes its 64 columns; the other 64 of the head, the log-sum-exp and all else stay within the bounds."""
+    D = 128
+    wl = _workload(Hq, Hkv, D, dt, q_scale)
+    host, bt, lens = _pool(wl)
+    rows, out, lse, bound, lse_bound = reference(wl.q, *host, bt, lens, wl.scale)
+    G = Hq // Hkv
+    bad = {(0, 0): (1700, 1), (2, 0): (39, 0), (3, Hkv - 1): (12345, 0), (4, 0): (0, 1)}  # (token, group)
+    for (b, kvh), (t, grp) in bad.items():
+        host[3][bt[b][t // 32], kvh, t % 32, grp, 0] = value
+        host[3][bt[b][t // 32], kvh, t % 32, grp, 1] = 0.0 if value == INF else NAN
+        if value == INF:
+            host[1][bt[b][t // 32], kvh, t % 32] = 0
+    cache = to_device(*host, wl.q.dtype)
+    lost = np.zeros(out.shape, dtype=bool)
+    other = np.zeros(out.shape, dtype=bool)  # the spoilt row's other group: its codes were changed (an infinity's case)
+    for i, (b, h) in enumerate(rows):
+        if (b, h // G) in bad:
+            grp = bad[b, h // G][1]
+            lost[i, 64 * grp : 64 * grp + 64] = True
+            other[i, 64 * (1 - grp) : 64 * (1 - grp) + 64] = True
+    if value == INF:  # the reference of the other group, with the codes as they are now
+        fine = [x.copy() for x in host]
+        fine[3][~np.isfinite(fine[3])] = 0.0
+        _, out2, _, bound2, _ = reference(wl.q, *fine, bt, lens, wl.scale)
+        out, bound = np.where(other, out2, out), np.where(other, bound2, bound)
+    for ns in (0, 1, 7, 300):
+        got_lse = torch.zeros(len(LENS), Hq, device="cuda")
+        got = pa.decode_int4(wl.q.cuda(), *cache, torch.from_numpy(bt).cuda(), torch.from_numpy(lens).cuda(), max(LENS),
+                             wl.scale, lse=got_lse, num_partitions=ns)
+        at = np.asarray(rows)
+        o, l = (x.double().cpu().numpy()[at[:, 0], at[:, 1]] for x in (got, got_lse))
+        assert not np.isfinite(o[lost]).any(), ns
+        assert_within(o[~lost], out[~lost], bound[~lost], f"beside {value} in V, partitions {ns}")
+        assert_within(l, lse, lse_bound, f"beside {value} in V, partitions {ns}, lse")
