@@ -414,7 +414,9 @@ int pa_load_blocks_int4(const int32_t* pairs, int num_pairs, const void* k_codes
 /* different sizes one after another.                                       */
 /* Internally q enters as fp16 after an exact power-of-two prescale (its    */
 /* largest magnitude lands in [2^14, 2^15)) and the softmax weights enter   */
-/* the V product times the V scale, as fp16.  The matrix unit cuts what a   */
+/* the V product times the V scale, as fp16: in two terms (2^-22) where     */
+/* dtype is fp16, rounded once (2^-11, under a bf16 output's own rounding)  */
+/* where it is bf16.  The matrix unit cuts what a                           */
 /* q element adds to a score at about 2^-18 of the largest q of the 16 it   */
 /* adds up at once, per unit of a code: q elements 2^7 times smaller than   */
 /* that still count to 11 bits, those 2^18 times smaller not at all; below  */

@@ -35,9 +35,14 @@
 //     through shared memory: s_K times the score scale as fp32, s_V as fp32, both z as fp16.
 //   * Scores: s_t = sum_group s_K (sum code q + z_K sum q).  The zero-point part is one more product per group, of z
 //     (times 2^-6: below 2^-8 it loses bits worth 2^-19 of a code) with the group sum of q in two fp16 terms.
-//   * PV: the weight of a token enters times its V scale, P' = 2^(x - R) s_V in fp16 (rounded once, 2^-11).  The
-//     zero-point part is again one product per group, of z_V with the same P', so code and zero-point parts carry
-//     the same rounding and the error stays relative to the value, not to the code.
+//   * PV: the weight of a token enters times its V scale, P' = 2^(x - R) s_V, in fp16.  The zero-point part is again one
+//     product per group, of z_V with the same P', so code and zero-point parts carry the same rounding and the error
+//     stays relative to the value, not to the code.  Rounded once (2^-11), P' adds an error as large as an fp16 output's
+//     own rounding: against 64 bits 2.9e-4 where that rounding alone leaves 2.05e-4 (64 sequences of 1 to 64 tokens).
+//     So where the output is fp16 P' enters in two terms (2^-22; 2.05e-4): up to 4 heads leave half of the products'
+//     columns free for the second term (128 sequences of 100 to 1024, 16 heads, 22.7 -> 23.8 us), 8 heads take products of
+//     their own (64 of 4096 to 8192, 64 heads, 98 -> 110 us).  A bf16 output's rounding leaves 1.65e-3, and one term makes
+//     it 1.66e-3: one term.
 //   * Online softmax with a reference R per head that moves only when it must: a piece starts with a guess, which
 //     stays if it puts the first tile's largest P' into [2^3, 2^15) and is set so (to (2^3, 2^4]) otherwise; later R
 //     is raised only when P' come near 2^15 or the sum l passes 2^100.  Any R gives the same quotient O / l;
@@ -46,7 +51,7 @@
 // Measured (B200): 64 sequences of 4096 to 8192 tokens, 64 heads, 8 KV heads of 128 (455 MB): 92 us, 4.9 TB/s, in bursts,
 // 101 to 105 at the power limit; the tiles go by at 6 TB/s.  128 sequences of 100 to 1024, 16 heads (84 MB): 22.4 us, of which
 // 3 until the first loads, 2 until they land, 14 at 6 TB/s and 2 to 3 until the last CTA has joined its pieces.  One sequence
-// of 100001, 32 heads, 2 KV heads: 23.3 us.  4 sequences of up to 64 tokens: 3.8 us.
+// of 100001, 32 heads, 2 KV heads, fp16: 26.3 us.  4 sequences of up to 64 tokens, fp16: 3.95 us.
 
 #include <algorithm>
 #include <atomic>
@@ -236,6 +241,9 @@ constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;  // a nibble of each
 template <int DT, int D, int G>
 struct State {
   static constexpr int NG = D / 64, KS = D / 16, WPL = D / 32;  // WPL: K words a lane reads of a row
+  // Where the output is fp16, a weight times its V scale enters in two fp16 terms.  Up to 4 heads leave columns free:
+  // columns 4 to 7 are the same heads once more, with the second terms (SIDE); 8 heads take products of their own (TWICE).
+  static constexpr bool SIDE = DT == PA_F16 && G <= 4, TWICE = DT == PA_F16 && G > 4;
   uint32_t qb[KS][2];  // q as B operand (fp16, prescaled)
   uint32_t qsum[NG];   // B operand of the zero-point product: lanes c = 0 the sum of q over a group, 2^-14 of it in two terms
   float o[KS][4];      // O^T times 2^-24 (rows g) and 2^-20 (rows g + 8), columns heads
@@ -257,8 +265,9 @@ struct State {
       // stored word WPL * c + i of a row: 8 values from `base` on
       const int base = D == 128 ? 64 * (i & 1) + 8 * (2 * c + (i >> 1)) : 8 * (2 * c + i);
       raw[i] = make_uint4(0, 0, 0, 0);
-      if (g < G) {
-        const uint4* at = reinterpret_cast<const uint4*>(qrows + (g * D + base) * 2);
+      const int h = SIDE ? g & 3 : g;
+      if (h < G) {
+        const uint4* at = reinterpret_cast<const uint4*>(qrows + (h * D + base) * 2);
         raw[i] = in_shared ? *at : __ldcg(at);
       }
     }
@@ -354,7 +363,9 @@ struct State {
       float any = set ? 1.f : 0.f;
       u = rows_max(u);
       v = rows_max(v);
-      set = rows_max(any) > 0.f;
+      any = rows_max(any);
+      if constexpr (SIDE) any = fmaxf(any, __shfl_xor_sync(0xffffffffu, any, 2));  // and both columns of a head
+      set = any > 0.f;
       float up = fmaxf(u - 4.f, v - 90.f);
       if (set) up = fmaxf(up, 0.f);
       else if (u == -INFINITY) up = v, still = true;
@@ -489,7 +500,8 @@ struct State {
         sv[r][0] = a[0];
       }
     }
-    uint32_t pk[NG][4];
+    uint32_t pk[NG][4], pl[NG][4];  // the weights (TWICE: their first terms), their second terms
+    const uint32_t second = SIDE && c >= 2 ? 0xffffffffu : 0u;
     float sum[2];
     for (bool moved = false;; moved = true) {
       bool move = false;
@@ -500,7 +512,14 @@ struct State {
         sum[0] += p0;
         sum[1] += p1;
 #pragma unroll
-        for (int grp = 0; grp < NG; ++grp) pk[grp][r] = pack_h2(p0 * sv[r][grp], p1 * sv[r][grp]);
+        for (int grp = 0; grp < NG; ++grp) {
+          const float a = p0 * sv[r][grp], b = p1 * sv[r][grp];
+          pk[grp][r] = pack_h2(a, b);
+          if constexpr (SIDE || TWICE) {
+            const float2 first = __half22float2(as_h2(SIDE ? pk[grp][r] & second : pk[grp][r]));
+            (SIDE ? pk : pl)[grp][r] = pack_h2(a - first.x, b - first.y);
+          }
+        }
       }
       // each P' is at most the lane's sum times the largest scale: below 2^15, and l below 2^100
 #pragma unroll
@@ -519,7 +538,7 @@ struct State {
           for (int r = 0; r < 4; ++r) top = __hmax2(top, as_h2(pk[grp][r]));
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) top = __hmax2(top, as_h2(__shfl_xor_sync(0xffffffffu, as_u32(top), o)));
-        low |= !(__low2float(top) >= 8.f) || !(__high2float(top) >= 8.f);
+        low |= (!SIDE || c < 2) && (!(__low2float(top) >= 8.f) || !(__high2float(top) >= 8.f));
         move = __any_sync(0xffffffffu, low);
         fresh = move;
       }
@@ -536,7 +555,10 @@ struct State {
 #pragma unroll
     for (int grp = 0; grp < NG; ++grp)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) pk[grp][r] = trans8x8(pk[grp][r]);  // tokens along the rows of the B operand
+      for (int r = 0; r < 4; ++r) {  // tokens along the rows of the B operand
+        pk[grp][r] = trans8x8(pk[grp][r]);
+        if constexpr (TWICE) pl[grp][r] = trans8x8(pl[grp][r]);
+      }
     // ---- O^T += V^T P'^T: tokens 2c, 2c + 1, 2c + 8, 2c + 9 of each half; word `grp` of lane g's piece of a row holds
     // values 64 grp + 8 g ..
     // (codes lie swizzled, see bring; odd c take their two tokens in the other order, which with the swizzle spreads
@@ -568,8 +590,11 @@ struct State {
         for (int grp = 0; grp < NG; ++grp) zp[hh][grp] = a[grp];
       }
 #pragma unroll
-      for (int grp = 0; grp < NG; ++grp)
+      for (int grp = 0; grp < NG; ++grp) {
         mma_f16(z[grp], zp[0][grp], zp[0][grp], zp[1][grp], zp[1][grp], pk[grp][2 * mt], pk[grp][2 * mt + 1]);
+        if constexpr (TWICE)
+          mma_f16(z[grp], zp[0][grp], zp[0][grp], zp[1][grp], zp[1][grp], pl[grp][2 * mt], pl[grp][2 * mt + 1]);
+      }
 #pragma unroll
       for (int grp = 0; grp < NG; ++grp)
 #pragma unroll
@@ -581,15 +606,28 @@ struct State {
             const uint32_t as = a >> (8 * s), bs = b >> (8 * s);
             mma_f16(o[4 * grp + 2 * half + s], as & kLow, as & kHigh, bs & kLow, bs & kHigh,
                     pk[grp][2 * mt], pk[grp][2 * mt + 1]);
+            if constexpr (TWICE)
+              mma_f16(o[4 * grp + 2 * half + s], as & kLow, as & kHigh, bs & kLow, bs & kHigh,
+                      pl[grp][2 * mt], pl[grp][2 * mt + 1]);
           }
         }
     }
   }
 
-  // Completes the lanes' parts of l.
+  // Completes the lanes' parts of l, and adds up the terms that lie side by side.
   __device__ __forceinline__ void finish() {
 #pragma unroll
     for (int e = 0; e < 2; ++e) l[e] = rows_sum(l[e]);
+    if constexpr (SIDE) {
+#pragma unroll
+      for (int i = 0; i < KS; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][e] += __shfl_xor_sync(0xffffffffu, o[i][e], 2);
+#pragma unroll
+      for (int grp = 0; grp < NG; ++grp)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) z[grp][e] += __shfl_xor_sync(0xffffffffu, z[grp][e], 2);
+    }
   }
   // The 8 output values 64 grp + 8 g .. of head 2c + e, relative to R.
   __device__ __forceinline__ void values(int grp, int e, float (&v)[8]) const {
