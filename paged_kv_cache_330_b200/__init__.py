@@ -21,6 +21,7 @@ Calls (see the header for exact semantics):
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 
 import numpy as np
@@ -598,6 +599,14 @@ def _made_for(stream, make, *args, **kw):
         return make(*args, **kw)
 
 
+def _refuse(stream, tensors):
+    """The words for a call that the native module refused although types, shapes and numbers are right."""
+    try:
+        _device_slow(stream, tensors)
+    except AssertionError:
+        raise ValueError("an argument is not as this call takes it (sizes below 2^31, plain dense tensors)") from None
+
+
 def _int4_caches(k_codes, v_codes, k_params, v_params):
     """Codes uint8 [NB, Hkv, bs, D/2] (both alike), parameters [NB, Hkv, bs, D/64, 2] (both alike, bf16 or fp16):
     words what is wrong with them, if anything is; returns (NB, bs, Hkv, D)."""
@@ -629,7 +638,7 @@ def write_kv_int4(k, v, slot_mapping, k_codes, v_codes, k_params, v_params, k_ou
             if x is not None:
                 _want(name, x, dtype=k_params.dtype, shape=(T, Hkv, D))
         _want("slot_mapping", slot_mapping, dtype=torch.int64, shape=(T,))
-        _device_slow(stream, (k, v, slot_mapping, k_codes, v_codes, k_params, v_params, k_out, v_out))
+        _refuse(stream, (k, v, slot_mapping, k_codes, v_codes, k_params, v_params, k_out, v_out))
     if st:
         _check(st, "pa_write_kv_int4")
 
@@ -659,7 +668,7 @@ def rope_write_kv_int4(q, k, v, positions, cos_table, sin_table, slot_mapping, k
         _want("cos_table", cos_table, dtype=torch.float32, ndim=2)
         _want("cos_table", cos_table, shape=(cos_table.shape[0], D // 2))
         _want("sin_table", sin_table, dtype=torch.float32, shape=cos_table.shape)
-        _device_slow(stream, (q, q_out, k, v, positions, cos_table, sin_table, slot_mapping, k_codes, v_codes, k_params,
+        _refuse(stream, (q, q_out, k, v, positions, cos_table, sin_table, slot_mapping, k_codes, v_codes, k_params,
                               v_params, k_out, v_out))
     if st:
         _check(st, "pa_rope_write_kv_int4")
@@ -675,7 +684,7 @@ def copy_blocks_int4(pairs, k_codes, v_codes, k_params, v_params, stream=None) -
         _contig(pairs)
         _want("pairs", pairs, dtype=_torch().int32, ndim=2)
         _want("pairs", pairs, shape=(pairs.shape[0], 2))
-        _device_slow(stream, (pairs, k_codes, v_codes, k_params, v_params))
+        _refuse(stream, (pairs, k_codes, v_codes, k_params, v_params))
     if st:
         _check(st, "pa_copy_blocks_int4")
 
@@ -694,7 +703,7 @@ def load_blocks_int4(pairs, k_codes, v_codes, k_params, v_params, k_cache, v_cac
         _want("v_cache", v_cache, dtype=k_params.dtype, shape=k_cache.shape)
         _want("pairs", pairs, dtype=_torch().int32, ndim=2)
         _want("pairs", pairs, shape=(pairs.shape[0], 2))
-        _device_slow(stream, (pairs, k_codes, v_codes, k_params, v_params, k_cache, v_cache))
+        _refuse(stream, (pairs, k_codes, v_codes, k_params, v_params, k_cache, v_cache))
     if st:
         _check(st, "pa_load_blocks_int4")
 
@@ -718,7 +727,8 @@ def decode_int4(q, k_codes, v_codes, k_params, v_params, block_tables, context_l
     st = call(q, k_codes, v_codes, k_params, v_params, block_tables, context_lens, max_context_len, scale, out, lse,
               workspace, num_partitions, handle)
     if st == _NEEDS_WORKSPACE:  # zero-filled once; every call leaves it zeroed again (a given one the library checks)
-        need = decode_int4_plan(q.shape[0], q.shape[1], k_codes.shape[1], q.shape[2], max_context_len, num_partitions)[2]
+        need = decode_int4_plan(q.shape[0], q.shape[1], k_codes.shape[1], q.shape[2], operator.index(max_context_len),
+                                operator.index(num_partitions))[2]
         workspace = _made_for(stream, _torch().zeros, need, dtype=_torch().uint8, device=q.device)
         st = call(q, k_codes, v_codes, k_params, v_params, block_tables, context_lens, max_context_len, scale, out, lse,
                   workspace, num_partitions, handle)
@@ -736,10 +746,13 @@ def decode_int4(q, k_codes, v_codes, k_params, v_params, block_tables, context_l
         if lse is not None:
             _want("lse", lse, dtype=torch.float32, shape=(B, Hq))
         for name, x in (("max_context_len", max_context_len), ("num_partitions", num_partitions)):
-            if not -(1 << 31) <= int(x) < 1 << 31:
+            if not hasattr(x, "__index__"):
+                raise TypeError(f"{name} must be an integer, got {x!r}")
+            if not -(1 << 31) <= operator.index(x) < 1 << 31:
                 raise ValueError(f"{name} must fit in 32 bits, got {x}")
-        float(scale)
-        _device_slow(stream, (q, k_codes, v_codes, k_params, v_params, block_tables, context_lens, out, lse, workspace))
+        if not (hasattr(scale, "__float__") or hasattr(scale, "__index__")):
+            raise TypeError(f"scale must be a number, got {scale!r}")
+        _refuse(stream, (q, k_codes, v_codes, k_params, v_params, block_tables, context_lens, out, lse, workspace))
     if st:
         _check(st, "pa_decode_int4")
     return out
