@@ -575,7 +575,11 @@ def _native():
     if _NATIVE is None:
         import importlib
         _torch()  # the module links against torch's libraries
-        m = importlib.import_module("._calls", __name__)
+        try:
+            m = importlib.import_module("._calls", __name__)
+        except ImportError as e:
+            raise ImportError("the INT4 calls need the native module _calls.so, built against the installed torch: "
+                              "run paged_kv_cache_330_b200/build.py") from e
         m.bind(*(ctypes.cast(getattr(lib, f), _vp).value for f in _NATIVE_ENTRIES))
         _NATIVE = m
     return _NATIVE

@@ -5,8 +5,9 @@
 Each source compiles to an object under ``_build/`` (in parallel), then nvcc
 links the shared library next to this file.  ``binding/calls.cpp``, the native
 half of the Python binding, compiles to ``_calls.so`` against the installed
-torch's headers.  Nothing is JIT-compiled at import time: the binding loads the
-prebuilt libraries or fails.
+torch's headers; where there is no torch with headers the library is built
+without it (the C calls need no torch).  Nothing is JIT-compiled at import time:
+the binding loads the prebuilt libraries or fails.
 """
 
 from __future__ import annotations
@@ -54,7 +55,11 @@ def _compile(src: str, extra: list[str]) -> str:
 def _build_calls() -> None:
     """binding/calls.cpp -> _calls.so (host code only; torch is found without importing it)."""
     src = os.path.join(PKG, "binding", "calls.cpp")
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    spec = importlib.util.find_spec("torch")
+    torch = os.path.dirname(spec.origin) if spec and spec.origin else None
+    if torch is None or not os.path.isdir(os.path.join(torch, "include", "torch")):
+        sys.stderr.write("no torch with headers: _calls.so, which the INT4 calls from Python need, is not built\n")
+        return
     # the installed torch counts as a source: its headers fix the layout of a tensor
     deps = [src, os.path.join(INCLUDE, "paged_attn.h"), os.path.join(torch, "version.py")]
     if os.path.exists(CALLS) and all(os.path.getmtime(CALLS) >= os.path.getmtime(d) for d in deps):
@@ -76,13 +81,13 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
         calls = ex.submit(_build_calls)
         objs = list(ex.map(lambda s: _compile(s, extra if s.endswith(".cu") else []), srcs))
-        calls.result()
     newest = max(os.path.getmtime(o) for o in objs)
     if not os.path.exists(LIB) or os.path.getmtime(LIB) < newest:
         cmd = [NVCC, *ARCH, "-shared", "-o", LIB, *objs, "-cudart", "static"]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    calls.result()  # an error in the binding's half leaves the library built
     if verbose:
         print(f"built {LIB}")
     return LIB
