@@ -409,7 +409,8 @@ int pa_load_blocks_int4(const int32_t* pairs, int num_pairs, const void* k_codes
 /* rules and launch behaviour of pa_decode; the workspace size comes from   */
 /* pa_decode_int4_workspace_size (or pa_decode_int4_plan: grid = CTAs,      */
 /* max_pieces = partial results the workspace holds per head of a group),   */
-/* and num_partitions_or_0 above 1024 counts as 1024.  The counters lie     */
+/* and num_partitions_or_0 above 1024 counts as 1024.  max_blocks_per_seq * */
+/* block_size may be 2^31 - 1024 at most.  The counters lie                 */
 /* alike for all sizes: a workspace, zero-filled once, serves calls of      */
 /* different sizes one after another.                                       */
 /* Internally q enters as fp16 after an exact power-of-two prescale (its    */

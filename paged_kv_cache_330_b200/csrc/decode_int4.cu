@@ -1365,7 +1365,8 @@ extern "C" int pa_decode_int4(const void* q, const void* k_codes, const void* v_
   if ((int64_t)max_blocks_per_seq * block_size < max_context_len) return PA_ERR_INVALID;
   if (num_blocks == 0 && max_context_len > 0) return PA_ERR_INVALID;
   if ((int64_t)num_blocks * block_size >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
-  if ((int64_t)max_blocks_per_seq * block_size >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
+  // the kernel counts tokens in 32 bits, up to a window of look-ups (32 chunks of 16) past a sequence's end
+  if ((int64_t)max_blocks_per_seq * block_size > (1ll << 31) - 1024) return PA_ERR_UNSUPPORTED;
   if ((int64_t)num_kv_heads * block_size * head_dim >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
   Plan pl;
   if (!make_plan(batch, num_q_heads, num_kv_heads, head_dim, max_context_len, num_partitions_or_0, &pl))

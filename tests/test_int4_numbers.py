@@ -42,3 +42,17 @@ def test_numbers_of_other_kinds_reach_the_device_check(good):
 def test_a_refusal_without_a_known_reason_is_an_error_of_the_arguments():
     with pytest.raises(ValueError, match="not as this call takes it"):
         pa._refuse(None, ())
+
+
+def test_tables_of_nearly_2_to_the_31_tokens_are_refused():
+    """The kernel counts tokens in 32 bits, some hundreds past a sequence's end."""
+    def call(mb, bs):  # addresses that are never used; without a workspace the last check refuses what is left
+        at = 0x10000
+        return pa.lib.pa_decode_int4(at, at, at, at, at, at, mb, at, 2, 4, 2, 128, bs, 16, 100, 0.1, 1, None, 0, 0, at,
+                                     None, None)
+
+    for bs in (16, 256):
+        most = ((1 << 31) - 1024) // bs
+        assert call(most, bs) == -4       # PA_ERR_WORKSPACE
+        assert call(most + 1, bs) == -2   # PA_ERR_UNSUPPORTED
+        assert call((1 << 31) // bs - 1, bs) == -2
