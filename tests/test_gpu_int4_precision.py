@@ -6,7 +6,8 @@ import numpy as np
 import pytest
 import torch
 
-from tests.int4_common import quantized_pool, reference, to_device
+from oracle import kv_int4 as oq
+from tests.int4_common import assert_within, quantized_pool, reference, to_device
 from workloads import make_custom
 
 pytestmark = pytest.mark.gpu
@@ -45,3 +46,45 @@ def test_decode_int4_error_is_the_outputs_rounding(Hq, Hkv, D, dtype):
                              num_partitions=ns)
         err = np.linalg.norm(got.double().cpu().numpy().reshape(out.shape) - out)
         assert err <= 1.15 * own, (err / own, own / np.linalg.norm(out))
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,dtype", [(128, 8, 2, "bf16"), (64, 4, 4, "f16"), (128, 16, 1, "f16"), (64, 8, 4, "bf16")])
+def test_decode_int4_small_q_elements_beside_an_outlier_count(D, Hq, Hkv, dtype):
+    """One channel of q 2^8 times the others, K alike there for all tokens: what tells the tokens apart is what the
+    small elements add.  The matrix unit cuts each of the 16 products of a step at 2^-18 of the largest |q| of the 16, per
+    unit of a code: over D / 16 steps, of which one has the outlier, a score moves by at most
+    d2 = 16 2^-18 (|outlier| + (D / 16 - 1) m) s scale, m the largest of the other elements and s the sequence's largest
+    K scale.  On top of the bounds without outliers: 2 d2 (A + |ref|) for an element, d2 for a log-sum-exp.  Neither
+    zeros nor the result that only the outlier decides lie within them."""
+    wl = make_custom(seed=13, lens=[700, 33, 1024, 5, 3000], num_q_heads=Hq, num_kv_heads=Hkv, head_dim=D,
+                     block_size=16, dtype=dtype)
+    wl.q[..., 5] = 2.0 ** 8
+    wl.k_cache0[..., 5] = 1.0
+    _, bt, lens, _, _ = pa.replay_ops(wl.ops, wl.num_blocks, 16, wl.free_order, wl.batch)
+    (kc, kp), (vc, vp) = quantized_pool(wl.k_cache0), quantized_pool(wl.v_cache0)
+    rows, out, lse, bound, lse_bound = reference(wl.q, kc, vc, kp, vp, bt, lens, wl.scale)
+    only = torch.zeros_like(wl.q)
+    only[..., 5] = wl.q[..., 5]
+    _, dropped, _, _, _ = reference(only, kc, vc, kp, vp, bt, lens, wl.scale, want_bound=False)
+    q = wl.q.double().numpy()
+    for i, (b, h) in enumerate(rows):
+        L = int(lens[b])
+        blk, kvh = np.asarray(bt[b][: -(-L // 16)], dtype=np.int64), h // (Hq // Hkv)
+        take = lambda a: a[blk, kvh].reshape(-1, *a.shape[3:])[:L].astype(a.dtype)  # noqa: E731
+        k, v = oq.values(take(kc), take(kp)), oq.values(take(vc), take(vp))
+        x = (k @ q[b, h]) * wl.scale
+        w = np.exp(x - x.max())
+        A = (w / w.sum()) @ np.abs(v)
+        m = np.abs(np.delete(q[b, h], 5)).max()
+        d2 = 16 * 2.0 ** -18 * (abs(q[b, h, 5]) + (D / 16 - 1) * m) * take(kp)[..., 0].max() * wl.scale
+        bound[i] += 2 * d2 * (A + np.abs(out[i]))
+        lse_bound[i] += d2
+    many = np.array([lens[b] > 5 for b, _ in rows])
+    for other in (np.zeros_like(out), dropped):
+        assert (np.abs(other - out) > bound)[many].mean() > 0.5
+    cache = to_device(kc, vc, kp, vp, wl.q.dtype)
+    got_lse = torch.empty(len(lens), Hq, device="cuda")
+    got = pa.decode_int4(wl.q.cuda(), *cache, torch.from_numpy(bt).cuda(), torch.from_numpy(lens).cuda(), 3000, wl.scale,
+                         lse=got_lse)
+    assert_within(got.double().cpu().numpy().reshape(out.shape), out, bound, "outlier in q")
+    assert_within(got_lse.double().cpu().numpy().reshape(-1), lse, lse_bound, "outlier in q, lse")
