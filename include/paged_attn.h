@@ -337,16 +337,20 @@ int pa_decode_int8(const void* q, const void* k_codes, const void* v_codes, cons
 /* in fp32 (IEEE division, multiply, subtract, each rounded), round16 and   */
 /* rint to nearest even.  Where s < 2^-126 (values all alike, or nearer     */
 /* than the type's scale can say): s = |lo|, z = sign(lo), codes 0.  The    */
-/* codes are taken against the rounded s and z, so those roundings cost at  */
-/* most a shifted range, never an inconsistent value.  4.5 bits per value.  */
+/* codes are taken against the rounded s and z: a value inside the range    */
+/* they span is off by s / 2 at most.  The roundings shift that range by up */
+/* to u (15 + |z|) s, u = 2^-8 (bf16) or 2^-11 (fp16); values beyond its    */
+/* ends are clamped and off by as much more.  That is less than s while     */
+/* |lo| is below 15 times hi - lo; bf16 groups of 300 +- 9 reach 1.1 s in   */
+/* all, of 1000 +- 9 3.8 s.  4.5 bits per value.                            */
 /* Finite values of any size are in the format.  A NaN or an infinity       */
 /* spoils its own group, all of it: min and max keep a NaN, so s is         */
 /* infinite or NaN and the group stands for nothing finite; other groups   */
 /* keep their values.                                                       */
 /* Layout: codes k_codes, v_codes uint8 [num_blocks][Hkv][block_size][D/2]  */
 /* (head-major, unlike the 16-bit and int8 caches: one head's rows of a     */
-/* block are one contiguous run that one bulk copy fetches).  A row is D/8  */
-/* 4-byte words of 8 codes, lowest nibble first; word j holds values        */
+/* block are one contiguous run).  A row is D/8 4-byte words of 8 codes,    */
+/* lowest nibble first; word j holds values                                 */
 /* 8 * (j div n) .. + 7 of group j mod n (the groups' words alternate, so   */
 /* that a thread's 16-byte load holds codes of every group).  Parameters    */
 /* k_params, v_params [num_blocks][Hkv][block_size][n][2] = (s, z), 16-bit  */
@@ -410,19 +414,20 @@ int pa_load_blocks_int4(const int32_t* pairs, int num_pairs, const void* k_codes
 /* pa_decode_int4_workspace_size (or pa_decode_int4_plan: grid = CTAs,      */
 /* max_pieces = partial results the workspace holds per head of a group),   */
 /* and num_partitions_or_0 above 1024 counts as 1024.  max_blocks_per_seq * */
-/* block_size may be 2^31 - 1024 at most.  The counters lie                 */
-/* alike for all sizes: a workspace, zero-filled once, serves calls of      */
-/* different sizes one after another.                                       */
+/* block_size may be 2^31 - 1024 at most.  The counters lie alike for all   */
+/* sizes: a workspace, zero-filled once, serves calls of different sizes    */
+/* one after another.                                                       */
 /* Internally q enters as fp16 after an exact power-of-two prescale (its    */
 /* largest magnitude lands in [2^14, 2^15)) and the softmax weights enter   */
 /* the V product times the V scale, as fp16: in two terms (2^-22) where     */
 /* dtype is fp16, rounded once (2^-11, under a bf16 output's own rounding)  */
-/* where it is bf16.  The matrix unit cuts what a                           */
-/* q element adds to a score at about 2^-18 of the largest q of the 16 it   */
-/* adds up at once, per unit of a code: q elements 2^7 times smaller than   */
-/* that still count to 11 bits, those 2^18 times smaller not at all; below  */
-/* 2^-28 of the largest finite q of its KV head's group an element loses    */
-/* bits of its own.  An infinity or NaN in q spoils its own head.           */
+/* where it is bf16.  The matrix unit cuts what a q element adds to a score */
+/* at about 2^-18 of the largest q of the 16 it adds up at once, per unit   */
+/* of a code: q elements 2^7 times smaller than that still count to 11      */
+/* bits, those 2^18 times smaller not at all; below 2^-28 of the largest    */
+/* finite q of its KV head's group an element loses bits of its own.  An    */
+/* infinity or NaN in q spoils its own head, one in a K row the heads that  */
+/* read it, one in a V row the 64 columns of its group.                     */
 /* Parameters not written by these calls: s >= 0, |z| < 65504.              */
 int pa_decode_int4_plan(int batch, int num_q_heads, int num_kv_heads, int head_dim, int max_context_len,
                         int num_partitions_or_0, int* grid_out, int* max_pieces_out, size_t* workspace_bytes_out);

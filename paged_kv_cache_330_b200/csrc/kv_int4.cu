@@ -14,8 +14,10 @@
 // in fp32, every operation rounded by itself (so another IEEE implementation
 // reaches the same codes).  The quotients are subtracted, not the values: hi -
 // lo can overflow, the difference of the quotients cannot.  s and z are rounded
-// before the codes are taken, so the rounding shifts the range the codes span
-// but adds nothing to a value's error.  s < 2^-126 (all values alike, or nearer
+// before the codes are taken, so a value inside the range the codes span is off
+// by half a step s; the rounding shifts that range by up to u (15 + |z|) steps
+// (u half a step of the type, 2^-8 or 2^-11), and values beyond its ends are
+// clamped and lose what was shifted.  s < 2^-126 (all values alike, or nearer
 // than the type can say; 1 / s would overflow): s = |lo|, z = sign(lo), codes 0.
 // One group never spans tokens: appending a token re-quantises nothing.  A NaN
 // in a group makes both extremes NaN, and s and z with them; an infinity makes s

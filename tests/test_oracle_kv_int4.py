@@ -105,3 +105,17 @@ def test_a_nan_or_infinity_spoils_its_group(dtype):
     assert not np.isfinite(held[lost]).any() and not np.isfinite(s[lost]).any() and (code[lost] == 0).all()
     assert np.array_equal(code[~lost], c0[~lost]) and np.array_equal(s[~lost], s0[~lost])
     assert np.array_equal(z[~lost], z0[~lost])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("offset", [0, 30, 300, 1000])
+def test_groups_far_from_zero_lose_what_the_rounding_shifts(dtype, offset):
+    """Within u (15 + |z|) steps more than half a step (and the arithmetic's 2^-22 of |x / s| and |z|); bf16 groups far
+    from zero do lose more than half a step at their ends, so the half step alone is no bound."""
+    g = torch.Generator().manual_seed(offset)
+    x = (offset + 3 * torch.randn(500, 1, 64, generator=g).clamp(-3, 3)).to(dtype)
+    code, s, z = oq.quantize_rows(x)
+    err, bound = _errors(x, s[..., None].astype(np.float64) * (code + z[..., None].astype(np.float64)), s, z)
+    assert (err <= bound).all()
+    if dtype == torch.bfloat16 and offset >= 300:
+        assert (err > 0.6 * s[..., None]).any()
