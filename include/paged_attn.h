@@ -427,7 +427,10 @@ int pa_load_blocks_int4(const int32_t* pairs, int num_pairs, const void* k_codes
 /* bits, those 2^18 times smaller not at all; below 2^-28 of the largest    */
 /* finite q of its KV head's group an element loses bits of its own.  An    */
 /* infinity or NaN in q spoils its own head, one in a K row the heads that  */
-/* read it, one in a V row the 64 columns of its group.                     */
+/* read it, one in a V row the 64 columns of its group.  A softmax weight   */
+/* times its V scale counts down to 2^-28 of the largest of its head, both  */
+/* groups of a row of 128 taken together: columns of a group whose V scales */
+/* are 2^17 and more below the other group's lose bits.                     */
 /* Parameters not written by these calls: s >= 0, |z| < 65504.              */
 int pa_decode_int4_plan(int batch, int num_q_heads, int num_kv_heads, int head_dim, int max_context_len,
                         int num_partitions_or_0, int* grid_out, int* max_pieces_out, size_t* workspace_bytes_out);

@@ -88,3 +88,35 @@ def test_decode_int4_small_q_elements_beside_an_outlier_count(D, Hq, Hkv, dtype)
                          lse=got_lse)
     assert_within(got.double().cpu().numpy().reshape(out.shape), out, bound, "outlier in q")
     assert_within(got_lse.double().cpu().numpy().reshape(-1), lse, lse_bound, "outlier in q, lse")
+
+
+@pytest.mark.parametrize("shift", [8, 14, 20, 27])
+@pytest.mark.parametrize("Hq,Hkv,small", [(8, 2, 0), (16, 1, 1), (2, 2, 1)])
+def test_decode_int4_groups_of_v_with_scales_far_apart(Hq, Hkv, small, shift):
+    """The values of one group 2^shift times smaller than those of the row's other group (bf16).  Both enter with one
+    power of two per head, so a weight times its V scale counts down to 2^-28 of the head's largest, T: the columns of the
+    small group are off by at most L 2^-28 T (15 + |z|) more than the usual bound.  The other group's columns, and the
+    log-sum-exps, keep the usual bounds."""
+    D, lens = 128, [700, 33, 1024, 5, 1]
+    wl = make_custom(seed=31 + shift, lens=lens, num_q_heads=Hq, num_kv_heads=Hkv, head_dim=D, block_size=16)
+    wl.v_cache0[..., 64 * small : 64 * small + 64] *= 2.0 ** -shift
+    _, bt, ln, _, _ = pa.replay_ops(wl.ops, wl.num_blocks, 16, wl.free_order, wl.batch)
+    (kc, kp), (vc, vp) = quantized_pool(wl.k_cache0), quantized_pool(wl.v_cache0)
+    rows, out, lse, bound, lse_bound = reference(wl.q, kc, vc, kp, vp, bt, ln, wl.scale)
+    q = wl.q.double().numpy()
+    for i, (b, h) in enumerate(rows):
+        L = int(ln[b])
+        blk, kvh = np.asarray(bt[b][: -(-L // 16)], dtype=np.int64), h // (Hq // Hkv)
+        take = lambda a: a[blk, kvh].reshape(-1, *a.shape[3:])[:L]  # noqa: E731
+        x = (oq.values(take(kc), take(kp)) @ q[b, h]) * wl.scale
+        w = np.exp(x - x.max()) / np.exp(x - x.max()).sum()
+        par = take(vp).astype(np.float64)
+        T = (w[:, None] * par[..., 0]).max()
+        bound[i, 64 * small : 64 * small + 64] += L * 2.0 ** -28 * T * (15 + np.abs(par[:, small, 1]).max())
+    cache = to_device(kc, vc, kp, vp, wl.q.dtype)
+    got_lse = torch.empty(len(lens), Hq, device="cuda")
+    for ns in (0, 7):
+        got = pa.decode_int4(wl.q.cuda(), *cache, torch.from_numpy(bt).cuda(), torch.from_numpy(ln).cuda(), 1024, wl.scale,
+                             lse=got_lse, num_partitions=ns)
+        assert_within(got.double().cpu().numpy().reshape(out.shape), out, bound, f"groups 2^{shift} apart")
+        assert_within(got_lse.double().cpu().numpy().reshape(-1), lse, lse_bound, f"groups 2^{shift} apart, lse")
