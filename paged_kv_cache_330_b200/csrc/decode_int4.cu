@@ -40,18 +40,19 @@
 //     stays relative to the value, not to the code.  Rounded once (2^-11), P' adds an error as large as an fp16 output's
 //     own rounding: against 64 bits 2.9e-4 where that rounding alone leaves 2.05e-4 (64 sequences of 1 to 64 tokens).
 //     So where the output is fp16 P' enters in two terms (2^-22; 2.05e-4): up to 4 heads leave half of the products'
-//     columns free for the second term (128 sequences of 100 to 1024, 16 heads, 22.7 -> 23.8 us), 8 heads take products of
-//     their own (64 of 4096 to 8192, 64 heads, 98 -> 110 us).  A bf16 output's rounding leaves 1.65e-3, and one term makes
-//     it 1.66e-3: one term.
+//     columns free for the second term (128 sequences of 100 to 1024, 16 heads, 22.4 -> 23.4 us), 8 heads take products of
+//     their own (one sequence of 100001, 32 heads, 23.1 -> 24.9; 64 of 4096 to 8192, 64 heads, 90 -> 108 to 112: 60
+//     products a tile for 40, of 8 cycles each).  A bf16 output's rounding leaves 1.65e-3, and one term makes it 1.66e-3:
+//     one term.
 //   * Online softmax with a reference R per head that moves only when it must: a piece starts with a guess, which
 //     stays if it puts the first tile's largest P' into [2^3, 2^15) and is set so (to (2^3, 2^4]) otherwise; later R
 //     is raised only when P' come near 2^15 or the sum l passes 2^100.  Any R gives the same quotient O / l;
 //     the usual tile needs no maximum, no shuffles and no rescaling of O, one vote tells.  l and O are fp32.
 //
-// Measured (B200): 64 sequences of 4096 to 8192 tokens, 64 heads, 8 KV heads of 128 (455 MB): 92 us, 4.9 TB/s, in bursts,
-// 101 to 105 at the power limit; the tiles go by at 6 TB/s.  128 sequences of 100 to 1024, 16 heads (84 MB): 22.4 us, of which
+// Measured (B200): 64 sequences of 4096 to 8192 tokens, 64 heads, 8 KV heads of 128 (455 MB): 91 to 95 us, 4.9 TB/s, in
+// bursts, 102 to 106 at the power limit; the tiles go by at 6 TB/s.  128 sequences of 100 to 1024, 16 heads (84 MB): 22.4 us, of which
 // 3 until the first loads, 2 until they land, 14 at 6 TB/s and 2 to 3 until the last CTA has joined its pieces.  One sequence
-// of 100001, 32 heads, 2 KV heads, fp16: 26.3 us.  4 sequences of up to 64 tokens, fp16: 3.95 us.
+// of 100001, 32 heads, 2 KV heads, fp16: 24.9 us.  4 sequences of up to 64 tokens, fp16: 3.95 us.
 
 #include <algorithm>
 #include <atomic>
@@ -1257,7 +1258,8 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_int4_kernel(const Params p)
 // 64 sequences of 500 to 8000).  A third stage changes nothing.  (Measured with K's codes low in their halves and segments cut.)
 // G 16 as one piece (two column tiles, 8 warps of 250 registers) against two halves on two CTAs: one sequence of 2000
 // tokens 14.7 and 11.3 us, of 100001 26.8 and 23.7, 16 of 8000 26.6 and 25.6, 64 of 100 to 8000 38.7 and 40.1 (D 128, 2
-// KV heads; D 64 10.3 and 9.8 to 27.7 and 29.4).  Halves, for all.
+// KV heads; D 64 10.3 and 9.8 to 27.7 and 29.4).  Halves for all sizes: they win where segments are few, by up to 23 %, and
+// lose up to 6 % where they are many; one form keeps one set of kernels.  (Measured with one term of the weights.)
 constexpr int kWarps = 12;
 
 template <int D, int G>
