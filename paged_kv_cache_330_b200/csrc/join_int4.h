@@ -48,9 +48,9 @@ struct Round {
   bool again;  // the joint share counts in the next round (else it is the segment's result)
 };
 
-// Round 0 or 1 of cut segment k as CTA `cta`, which holds a share of it, takes part in it.  A segment with many
-// shares is joined by groups of kGroup CTAs first (one SM reads shares at little more than 100 GB/s): round 0 joins the
-// shares of cta's group, round 1 the groups' joint shares.
+// The join of cut segment k as CTA `cta`, which holds a share of it, takes part in it: its first round (0) or its last (1).
+// A segment with many shares is joined by groups of kGroup CTAs first (one SM reads shares at little more than 100 GB/s):
+// the first round joins the shares of cta's group, the last the groups' joint shares.
 // Counters [3 kMaxGrid]: a CTA holds the first tile of one cut segment at most, so the segment's own counter is that
 // of its first CTA; and a later share of one segment at most, so a group's is that of its first CTA, apart where the
 // group starts with the segment's first share.
